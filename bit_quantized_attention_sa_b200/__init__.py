@@ -17,6 +17,8 @@ _BINDING_NAMES = (
     "sa_quantize_qk", "sa_quantize_v", "sa_attn_fwd", "sa_attn_fwd_quantized",
     "sa_debug_qk_s32", "sa_get_device_status", "sa_status_string", "sa_workspace_bytes",
     "sa_release_workspace", "SAError", "library_path",
+    "sa_rope_frequencies", "sa_rope", "SACache", "sa_cache_alloc", "sa_cache_append",
+    "sa_cache_read", "sa_cache_attn",
 )
 
 

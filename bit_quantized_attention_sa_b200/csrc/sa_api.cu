@@ -415,6 +415,47 @@ static void varlen_groups(int nseq, const int *seqlens, int H, std::vector<int> 
     }
 }
 
+// ------------------------------------------------------------------ cache calls
+
+static bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// What the calls on the cache share: sizes, the cache's and the sequences' arrays.
+static sa_status check_cache(int64_t T, int B, int H, int d, int max_pages, int num_pages, const void *tok_start,
+                             const void *kv_lens, const void *table, const void *k_codes, const void *k_scale,
+                             const void *v_codes, const void *v_scale)
+{
+    if (T < 0 || B < 1 || H < 1 || max_pages < 1 || num_pages < 1) return SA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return SA_ERR_UNSUPPORTED;
+    // lines of 128 bytes are a 32-bit TMA coordinate; positions and grid dimensions likewise
+    if (T > (1 << 30) || B > (1 << 20) || H > 65535 || max_pages > (1 << 30) / kPage ||
+        int64_t(num_pages) * H > (int64_t(INT_MAX) * 2) / d)
+        return SA_ERR_UNSUPPORTED;
+    if (T == 0) return SA_OK;
+    for (const void *p : {tok_start, kv_lens, table, k_codes, k_scale, v_codes, v_scale})
+        if (!p) return SA_ERR_INVALID_ARG;
+    if (!aligned16(k_codes) || !aligned16(v_codes)) return SA_ERR_MISALIGNED;
+    for (const void *p : {tok_start, kv_lens, table, k_scale, v_scale})
+        if (!aligned(p, 4)) return SA_ERR_MISALIGNED;
+    return SA_OK;
+}
+
+// A packed token tensor whose tokens have `width` values of 16 bits.
+static sa_status check_tokens(const void *p, int64_t stride, int64_t width)
+{
+    if (!p || stride < width) return SA_ERR_INVALID_ARG;
+    if (!aligned16(p) || stride % 8 != 0) return SA_ERR_MISALIGNED;
+    return SA_OK;
+}
+
+static int device_sms()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
 }  // namespace sa
 
 using namespace sa;
@@ -831,6 +872,214 @@ int sa_debug_varlen_groups(int nseq, const int *seqlens, int H, int *group_of)
     return int(groups.size());
 }
 
+sa_status sa_rope_frequencies(int rot, double base, int scaling, double factor, int original_len,
+                              double beta_fast, double beta_slow, double *freqs, float *amplitude)
+{
+    if (!freqs || !amplitude || rot < 16 || scaling < SA_ROPE_PLAIN || scaling > SA_ROPE_RAMP) return SA_ERR_INVALID_ARG;
+    if (rot % 16 != 0 || rot > 256) return SA_ERR_UNSUPPORTED;
+    if (!std::isfinite(base) || base <= 1.0 || !std::isfinite(factor) || factor < 1.0) return SA_ERR_INVALID_ARG;
+    const bool ramp = scaling == SA_ROPE_RAMP;
+    if (ramp && (original_len < 1 || !std::isfinite(beta_fast) || !(beta_fast > beta_slow) || !(beta_slow > 0.0)))
+        return SA_ERR_INVALID_ARG;
+    if (scaling == SA_ROPE_BASE) base *= std::pow(factor, double(rot) / (rot - 2));
+    // the (real) pair index that turns `turns` times within original_len positions
+    auto pair_of = [&](double turns) {
+        return rot * std::log(original_len / (turns * 2.0 * 3.14159265358979323846)) / (2.0 * std::log(base));
+    };
+    double lo = 0.0, hi = 0.0;
+    if (ramp) {
+        lo = std::max(0.0, std::floor(pair_of(beta_fast)));
+        hi = std::min(rot / 2 - 1.0, std::ceil(pair_of(beta_slow)));
+        hi = std::max(hi, lo + 1e-3);  // a step, where both borders fall on one pair
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == SA_ROPE_LINEAR) {
+            freqs[i] = f / factor;
+        } else if (ramp) {
+            const double share = std::min(1.0, std::max(0.0, (i - lo) / (hi - lo)));  // of the slowed frequency
+            freqs[i] = f * (1.0 - share) + f / factor * share;
+        } else {
+            freqs[i] = f;
+        }
+    }
+    *amplitude = ramp ? float(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return SA_OK;
+}
+
+sa_status sa_rope(const sa_rope_tensor *tensors, int count, int dtype, int B, int N, int d, int rot,
+                  int interleaved, const int32_t *pos, int64_t pos_axis, int64_t pos_batch, int axes,
+                  const int *sections, const double *freqs, float amplitude, int inverse, void *stream)
+{
+    if (!tensors || count < 1 || count > 2 || dtype < SA_BF16 || dtype > SA_FP32) return SA_ERR_INVALID_ARG;
+    if (B < 0 || N < 0 || d < 16 || rot < 16 || rot > d || axes < 1) return SA_ERR_INVALID_ARG;
+    if (d % 16 != 0 || d > 256 || rot % 16 != 0 || axes > 4) return SA_ERR_UNSUPPORTED;
+    if (int64_t(B) * N > (1 << 30)) return SA_ERR_UNSUPPORTED;
+    if (!std::isfinite(amplitude) || (!sections && axes != 1)) return SA_ERR_INVALID_ARG;
+    RopeArgs a;
+    for (int i = 0; i < 3; ++i) a.axis_end[i] = rot / 2;
+    if (sections) {
+        int sum = 0;
+        for (int i = 0; i < axes; ++i) {
+            if (sections[i] < 0 || sections[i] > rot / 2) return SA_ERR_INVALID_ARG;
+            sum += sections[i];
+            if (i < 3) a.axis_end[i] = i < axes - 1 ? sum : rot / 2;
+        }
+        if (sum != rot / 2) return SA_ERR_INVALID_ARG;
+    }
+    if (B == 0 || N == 0) return SA_OK;
+    const int64_t per16 = dtype == SA_FP32 ? 4 : 8;
+    for (int i = 0; i < count; ++i) {
+        const sa_rope_tensor &t = tensors[i];
+        if (!t.x || !t.y || t.heads < 1) return SA_ERR_INVALID_ARG;
+        if (t.heads > 65535) return SA_ERR_UNSUPPORTED;
+        if (!aligned16(t.x) || !aligned16(t.y)) return SA_ERR_MISALIGNED;
+        for (int64_t st : {t.x_batch, t.x_head, t.x_tok, t.y_batch, t.y_head, t.y_tok})
+            if (st % per16 != 0) return SA_ERR_MISALIGNED;
+        a.io[i] = RopeIo{t.x, t.y, t.x_batch, t.x_head, t.x_tok, t.y_batch, t.y_head, t.y_tok, t.heads};
+    }
+    if (!pos || !freqs) return SA_ERR_INVALID_ARG;
+    if (!aligned(pos, 4) || !aligned(freqs, 8)) return SA_ERR_MISALIGNED;
+    const sa_status r = check_device();
+    if (r != SA_OK) return r;
+    a.B = B;
+    a.N = N;
+    a.d = d;
+    a.rot = rot;
+    a.interleaved = interleaved != 0;
+    a.inverse = inverse != 0;
+    a.pos = pos;
+    a.pos_axis_stride = pos_axis;
+    a.pos_batch_stride = pos_batch;
+    a.freqs = freqs;
+    a.amplitude = amplitude;
+    return launch_rope(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+static CacheArgs cache_args(int64_t T, const int32_t *tok_start, const int32_t *kv_lens, const int32_t *page_table,
+                            int B, int max_pages, const int8_t *k_codes, const float *k_scale, const int8_t *v_codes,
+                            const float *v_scale, int num_pages, int H, int d)
+{
+    CacheArgs a;
+    a.k_codes = const_cast<int8_t *>(k_codes);
+    a.v_codes = const_cast<int8_t *>(v_codes);
+    a.k_scale = const_cast<float *>(k_scale);
+    a.v_scale = const_cast<float *>(v_scale);
+    a.tok_start = tok_start;
+    a.kv_lens = kv_lens;
+    a.table = page_table;
+    a.T = int(T);
+    a.B = B;
+    a.H = H;
+    a.d = d;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    return a;
+}
+
+sa_status sa_cache_append(const void *k, const void *v, int dtype, int64_t T, int64_t k_tok, int64_t v_tok,
+                          const int32_t *tok_start, const int32_t *kv_lens, const int32_t *page_table, int B,
+                          int max_pages, int8_t *k_codes, float *k_scale, int8_t *v_codes, float *v_scale,
+                          int num_pages, int H, int d, void *stream)
+{
+    if (dtype != SA_BF16 && dtype != SA_FP16) return SA_ERR_INVALID_ARG;
+    sa_status r = check_cache(T, B, H, d, max_pages, num_pages, tok_start, kv_lens, page_table, k_codes, k_scale,
+                              v_codes, v_scale);
+    if (r != SA_OK || T == 0) return r;
+    if ((r = check_tokens(k, k_tok, int64_t(H) * d)) != SA_OK) return r;
+    if ((r = check_tokens(v, v_tok, int64_t(H) * d)) != SA_OK) return r;
+    if ((r = check_device()) != SA_OK) return r;
+    CacheArgs a = cache_args(T, tok_start, kv_lens, page_table, B, max_pages, k_codes, k_scale, v_codes, v_scale,
+                             num_pages, H, d);
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_tok;
+    a.v_stride = v_tok;
+    return launch_cache_append(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+sa_status sa_cache_read(void *k, void *v, int dtype, int64_t T, const int32_t *tok_start,
+                        const int32_t *kv_lens, const int32_t *page_table, int B, int max_pages,
+                        const int8_t *k_codes, const float *k_scale, const int8_t *v_codes,
+                        const float *v_scale, int num_pages, int H, int d, void *stream)
+{
+    if (dtype < SA_BF16 || dtype > SA_FP32) return SA_ERR_INVALID_ARG;
+    sa_status r = check_cache(T, B, H, d, max_pages, num_pages, tok_start, kv_lens, page_table, k_codes, k_scale,
+                              v_codes, v_scale);
+    if (r != SA_OK || T == 0) return r;
+    if (!k && !v) return SA_ERR_INVALID_ARG;
+    if ((k && !aligned16(k)) || (v && !aligned16(v))) return SA_ERR_MISALIGNED;
+    if ((r = check_device()) != SA_OK) return r;
+    CacheArgs a = cache_args(T, tok_start, kv_lens, page_table, B, max_pages, k_codes, k_scale, v_codes, v_scale,
+                             num_pages, H, d);
+    a.k = k;
+    a.v = v;
+    return launch_cache_read(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+// The query side of an attention call over the cache.
+static sa_status check_group(int64_t T, int H, int group)
+{
+    if (group < 1) return SA_ERR_INVALID_ARG;
+    if (int64_t(H) * group > 65535 || T * group > (1 << 30) || T * H * group > (int64_t(1) << 34))
+        return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T, int64_t q_tok,
+                        const int32_t *tok_start, const int32_t *kv_lens, const int32_t *page_table, int B,
+                        int max_pages, const int8_t *k_codes, const float *k_scale, const int8_t *v_codes,
+                        const float *v_scale, int num_pages, int H, int group, int d, int causal, int window,
+                        float sm_scale, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if ((dtype != SA_BF16 && dtype != SA_FP16) || window < 0 || !std::isfinite(sm_scale) || sm_scale <= 0.0f)
+        return SA_ERR_INVALID_ARG;
+    sa_status r = check_cache(T, B, H, d, max_pages, num_pages, tok_start, kv_lens, page_table, k_codes, k_scale,
+                              v_codes, v_scale);
+    if (r == SA_OK) r = check_group(T, H, group);
+    if (r != SA_OK || T == 0) return r;
+    if ((r = check_tokens(q, q_tok, int64_t(H) * group * d)) != SA_OK) return r;
+    if (!o || !workspace) return SA_ERR_INVALID_ARG;
+    if (!aligned16(o) || !aligned16(workspace) || !aligned(lse, 4)) return SA_ERR_MISALIGNED;
+    if ((r = check_device()) != SA_OK) return r;
+    if (workspace_bytes < sa_cache_attn_workspace_bytes(T, B, H, group, d)) return SA_ERR_INVALID_ARG;
+    CUtensorMap tm_k, tm_v;
+    const uint64_t lines = uint64_t(num_pages) * uint64_t(H) * uint64_t(d) / 2;  // of 128 bytes
+    if (!encode_tmap_2d_u8(&tm_k, k_codes, 128, lines, 128, 128, uint32_t(d / 2), CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d_u8(&tm_v, v_codes, 128, lines, 128, 128, uint32_t(d / 2), CU_TENSOR_MAP_SWIZZLE_128B))
+        return SA_ERR_CUDA;
+    CacheAttnArgs a;
+    a.q = q;
+    a.o = o;
+    a.lse = lse;
+    a.dtype = dtype;
+    a.q_stride = q_tok;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.tok_start = tok_start;
+    a.kv_lens = kv_lens;
+    a.table = page_table;
+    a.T = int(T);
+    a.B = B;
+    a.H = H;
+    a.G = group;
+    a.d = d;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.causal = causal != 0;
+    a.window = std::min(window, 1 << 30);
+    a.sm_scale = sm_scale;
+    return launch_cache_attn(tm_k, tm_v, a, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK
+                                                                                                       : SA_ERR_CUDA;
+}
+
+size_t sa_cache_attn_workspace_bytes(int64_t T, int B, int H, int group, int d)
+{
+    if (T < 0 || B < 1 || H < 1 || (d != 64 && d != 128) || check_group(T, H, group) != SA_OK) return 0;
+    const int sms = device_sms();
+    return sms < 1 ? 0 : cache_attn_workspace(sms, d);
+}
+
 sa_status sa_debug_qk_s32(const int8_t *q_i8, const int8_t *k_i8, int B, int H, int N, int d,
                           int32_t *s_out, void *stream)
 {
@@ -870,11 +1119,14 @@ sa_status sa_debug_mma_peak(int kind, int reps, void *stream)
 
 sa_status sa_get_device_status(void)
 {
-    int st = 0, st_w8a8 = 0, st_peak = 0, st_sla = 0;
-    if (read_and_clear_status(&st) != cudaSuccess || read_and_clear_w8a8_status(&st_w8a8) != cudaSuccess ||
+    int st = 0, st_w8a8 = 0, st_peak = 0, st_sla = 0, st_cache = 0, st_cattn = 0;
+    if (read_and_clear_cache_status(&st_cache) != cudaSuccess || read_and_clear_cache_attn_status(&st_cattn) != cudaSuccess ||
+        read_and_clear_status(&st) != cudaSuccess || read_and_clear_w8a8_status(&st_w8a8) != cudaSuccess ||
         read_and_clear_peak_status(&st_peak) != cudaSuccess || read_and_clear_sla_status(&st_sla) != cudaSuccess)
         return SA_ERR_CUDA;
-    return st == 0 && st_w8a8 == 0 && st_peak == 0 && st_sla == 0 ? SA_OK : SA_ERR_DEVICE_TIMEOUT;
+    if (st != 0 || st_w8a8 != 0 || st_peak != 0 || st_sla != 0 || st_cattn == SA_ERR_DEVICE_TIMEOUT)
+        return SA_ERR_DEVICE_TIMEOUT;
+    return st_cache == 0 && st_cattn == 0 ? SA_OK : SA_ERR_BAD_INDEX;
 }
 
 const char *sa_status_string(sa_status s)
@@ -888,6 +1140,7 @@ const char *sa_status_string(sa_status s)
     case SA_ERR_OOM: return "SA_ERR_OOM";
     case SA_ERR_DEVICE_TIMEOUT: return "SA_ERR_DEVICE_TIMEOUT";
     case SA_ERR_SCRATCH_LIMIT: return "SA_ERR_SCRATCH_LIMIT";
+    case SA_ERR_BAD_INDEX: return "SA_ERR_BAD_INDEX";
     }
     return "SA_ERR_UNKNOWN";
 }

@@ -1,0 +1,664 @@
+// sa_cache_attn.cu -- attention of few query rows over the paged INT8 cache for sm_100a.
+//
+// Rows of a (sequence, key/value head) are its query tokens times the query heads that share
+// the head, token-major; a tile is 16 rows, the M of one mma.  For every 64-token block j
+//     S = q . k8,   x = S * (scale_k[j] * sm_scale),   p = exp(x - m),
+//     acc = acc * alpha + (p * scale_v[j]) . v8,   l = l * alpha + sum p,
+// with m, l and acc in fp32; in the end o = acc / l and lse = m + log l.
+//
+// The codes are exact in fp16, and so is q after a power of two for each row (its exponent goes
+// into the row's score scale), so S has no rounding before its fp32 accumulator.  p times the
+// ratio of scale_v[j] to the largest scale_v so far (u) is rounded to fp16, 2^15 times itself:
+// at most 2^15, relative error 2^-12, and what is below 2^-29 of the row's largest weight falls
+// to fp16's subnormals.  acc is kept in units of u * 2^-15.
+//
+// What bounds it: reading 2 d bytes for each cached token and head.  So every warp is a worker
+// of its own with a ring of TMA tiles in shared memory (K and V of a block are 64 x d bytes
+// each), and the blocks of all (sequence, head, tile) segments, laid out one after another, are
+// cut into equal ranges, one for each worker, whatever the lengths.  A range may begin or end
+// inside a segment: such pieces go to the workspace as (acc, m, l) and combine_kernel joins
+// them in the order of the workers, so results do not depend on timing.
+//
+// The tiles arrive with TMA's 128-byte swizzle (16-byte chunk c of the 128-byte line r at
+// c ^ (r & 7)), which makes the 16-byte reads below free of bank conflicts at d = 128: the
+// contraction index of an mma may be permuted freely as long as both operands agree, and so
+// may the keys of a tile (scores and values) and the channels (columns of acc).
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sa_internal.h"
+#include "sa_ptx.cuh"
+
+namespace sa {
+
+__device__ int g_cache_attn_status;  // 0 = OK, 6 = a bounded wait expired, 8 = bad index
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 16;         // rows of a tile
+constexpr int kSlots = 3;         // ring slots of a warp, one K or V tile each
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPScale = 32768.0f;
+
+template <int D>
+struct Sizes {
+    static constexpr uint32_t kTile = 64 * D;  // bytes of a K or V tile
+    static constexpr uint32_t kOffBar = kWarps * kSlots * kTile;
+    static constexpr uint32_t kBytes = kOffBar + kWarps * kSlots * 8;
+    static constexpr uint32_t kAlloc = kBytes + 1024;
+    static constexpr int kPart = kRows * (D + 2);  // floats of a partial result
+};
+static_assert(Sizes<128>::kAlloc <= 227 * 1024, "shared memory per CTA");
+
+__device__ __forceinline__ void record(int what) { atomicMax(&g_cache_attn_status, what); }
+
+// A sequence as the kernels see it: `tiles` tiles of its rows for each head, `nb` blocks for
+// each tile, from block `lo` on.  Every segment has a block at least, so that some worker
+// writes its rows; blocks that a tile sees nothing of are passed over.
+struct Seq {
+    int ts, n, len, tiles, lo, nb;
+    __device__ int64_t blocks(int heads) const { return int64_t(heads) * tiles * nb; }
+};
+
+__device__ __forceinline__ Seq load_seq(const CacheAttnArgs &A, int b)
+{
+    Seq s;
+    s.ts = A.tok_start[b];
+    const int te = A.tok_start[b + 1];
+    s.len = A.kv_lens[b];
+    s.n = te - s.ts;
+    if (s.ts < 0 || te < s.ts || te > A.T || s.len < 0 || s.len > int64_t(A.max_pages) * kPage) {
+        record(8);
+        s.n = s.len = s.ts = 0;
+    }
+    s.tiles = (s.n * A.G + kRows - 1) / kRows;
+    s.lo = A.window > 0 ? max(0, s.len - s.n - A.window + 1) / kPage : 0;
+    s.nb = max(1, (s.len + kPage - 1) / kPage - s.lo);
+    return s;
+}
+
+__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+
+// two of four bytes u = code + 128 to fp16: 0x6400 + u is 1024 + u, less 1152 is the code
+__device__ __forceinline__ uint32_t bytes_to_h2(uint32_t u, uint32_t sel)
+{
+    const uint32_t p = __byte_perm(u, 0x64646464u, sel);
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    return h2(__hsub2(*reinterpret_cast<const __half2 *>(&p), bias));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_out(float a, float b, __nv_bfloat16)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_out(float a, float b, __half)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// four consecutive values of a row as floats
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&f)[4])
+{
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const __half *p, float (&f)[4])
+{
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+
+// One block of the flattened work, held by one lane of a worker's window of 32.
+struct Entry {
+    int b, seg, blk;   // sequence, head * tiles + tile, block of the sequence (absolute)
+    int line;          // first 128-byte line of its tiles in the cache
+    float sk, sv;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const CacheAttnArgs A)
+{
+    using S = Sizes<D>;
+    constexpr int kSteps = D / 16;   // k16 steps of q . k
+    constexpr int kQuads = D / 64;   // 16-byte chunks of a key row that a lane reads
+    constexpr int kNT = D / 8;       // n8 tiles of acc
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ int64_t prefix[kThreads + 1];
+    __shared__ int64_t warp_sum[kWarps];
+    __shared__ int abort_word[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;
+
+    // ---- the flattened work: thread t sums the sequences [t * per, (t + 1) * per)
+    const int per = (A.B + kThreads - 1) / kThreads;
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = int(threadIdx.x) * per + i;
+        if (b < A.B) mine += load_seq(A, b).blocks(A.H);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    uint8_t *ring = smem + warp * kSlots * S::kTile;
+    const uint32_t ring_addr = smem_u32(ring);
+    const uint32_t bars = smem_u32(smem) + S::kOffBar + uint32_t(warp * kSlots) * 8;
+    volatile int *abort_flag = &abort_word[warp];
+    if (lane == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(bars + 8 * i, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    prefix[threadIdx.x] = before + incl - mine;
+    if (threadIdx.x == kThreads - 1) prefix[kThreads] = before + incl;
+    __syncthreads();
+    const int64_t total = prefix[kThreads];
+
+    // ---- this worker's range [w * chunk, end)
+    const int workers = int(gridDim.x) * kWarps;
+    const int w = warp * int(gridDim.x) + int(blockIdx.x);
+    const int64_t chunk = (total + workers - 1) / workers;
+    const int64_t start = w * chunk;
+    const int count = int(max(int64_t(0), min(total, start + chunk) - start));
+    if (count == 0) {
+        if (lane == 0) A.meta[w] = make_int4(0, 0, 0, 0);
+        return;
+    }
+
+    // each lane's cursor: the sequence of flattened block start + lane (+ 32, ...)
+    int cb;
+    int64_t cbase;  // blocks before sequence cb
+    {
+        int t = 0;
+        for (int i = 0; i < kWarps; ++i)
+            t += __popc(__ballot_sync(0xffffffffu, prefix[i * 32 + lane] <= start));
+        cb = (t - 1) * per;  // threads without sequences share the last prefix: still its end
+        cbase = prefix[t - 1];
+    }
+    Seq cs = load_seq(A, min(cb, A.B - 1));
+    auto next_entry = [&](int64_t f) -> Entry {
+        Entry e;
+        while (cb < A.B && f >= cbase + cs.blocks(A.H)) {
+            cbase += cs.blocks(A.H);
+            ++cb;
+            if (cb < A.B) cs = load_seq(A, cb);
+        }
+        e.b = cb;
+        e.seg = 0;
+        e.blk = 0;
+        e.line = 0;
+        e.sk = e.sv = 0.0f;
+        if (cb >= A.B) return e;
+        const uint64_t rem = uint64_t(f - cbase);
+        e.seg = int(rem / uint32_t(cs.nb));
+        e.blk = cs.lo + int(rem - uint64_t(e.seg) * uint32_t(cs.nb));
+        if (e.blk * kPage < cs.len) {
+            const int page = A.table[int64_t(cb) * A.max_pages + e.blk], head = e.seg / cs.tiles;
+            if (page < 0 || page >= A.num_pages) {
+                record(8);
+                e.sk = e.sv = __int_as_float(0x7fffffff);
+            } else {
+                e.line = (page * A.H + head) * int(S::kTile / 128);
+                e.sk = A.k_scale[int64_t(page) * A.H + head];
+                e.sv = A.v_scale[int64_t(page) * A.H + head];
+            }
+        }
+        return e;
+    };
+    Entry cur = next_entry(start + lane), nxt = next_entry(start + 32 + lane);
+
+    // tile u of the worker (u = 2 * block + (0 K, 1 V)) goes to slot u % kSlots
+    auto issue = [&](int u, int first) {
+        const int i = (u >> 1) - first;
+        const int line = __shfl_sync(0xffffffffu, i < 32 ? cur.line : nxt.line, i & 31);
+        if ((u >> 1) < count && lane == 0) {
+            const uint32_t bar = bars + 8 * uint32_t(u % kSlots);
+            mbar_arrive_expect_tx(bar, S::kTile);
+            tma_load_2d(ring_addr + uint32_t(u % kSlots) * S::kTile, (u & 1) ? &tm_v : &tm_k, bar, 0, line);
+        }
+    };
+    __syncwarp();
+    for (int u = 0; u < kSlots; ++u) issue(u, 0);
+
+    bool ok = true;
+    int window = 0, done = 0;         // first block of `cur`, tiles consumed
+    int seg_b = -1, seg = -1;         // the open segment
+    int seg_i = 0, seg_blk = 0;       // the block of the worker it was opened at, its index in the sequence
+    bool split = false;               // this worker began a segment that goes on elsewhere
+    Seq sq{};
+    int head = 0, row0 = 0, tile_first = 0, tile_last = -1, all_first = 0, all_last = -1;
+    uint32_t qf[kSteps][4];
+    float row_c[2], m[2], l[2], acc[kNT][4], u_ref = 0.0f;
+    int row_first[2], row_last[2];
+
+    auto open_segment = [&](int b, int sg) {
+        if (b != seg_b) sq = load_seq(A, b);
+        head = sg / sq.tiles;
+        row0 = (sg - head * sq.tiles) * kRows;
+        const int rows = sq.n * A.G, pos0 = sq.len - sq.n;
+        auto first_of = [&](int i) { return A.window > 0 ? max(0, pos0 + i - A.window + 1) : 0; };
+        auto last_of = [&](int i) { return A.causal ? pos0 + i : sq.len - 1; };
+        const int i_lo = row0 / A.G, i_hi = min(rows - 1, row0 + kRows - 1) / A.G;
+        tile_first = first_of(i_lo);
+        all_first = first_of(i_hi);
+        all_last = last_of(i_lo);
+        tile_last = last_of(i_hi);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int rr = row0 + g + 8 * r, i = rr / A.G;
+            const bool valid = rr < rows;
+            row_first[r] = first_of(i);
+            row_last[r] = valid ? last_of(i) : -1;
+            float x[kQuads][16], top = 0.0f;
+            const T *src = static_cast<const T *>(A.q) + (int64_t(sq.ts) + i) * A.q_stride +
+                           int64_t(head * A.G + rr - i * A.G) * D;
+#pragma unroll
+            for (int j = 0; j < kQuads; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (valid) load4(src + 16 * (c + 4 * j) + 4 * k, f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[j][4 * k + e] = f[e];
+                        top = fmaxf(top, fabsf(f[e]));
+                    }
+                }
+            // bf16 has more range than fp16: each row is brought to [1, 4) by a power of two,
+            // exactly; what leaves fp16's normal range then is below 2^-14 of the row's largest
+            float up = 1.0f, down = 1.0f;
+            if (sizeof(T) == 2 && A.dtype == 0) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                int ex = int(__float_as_uint(top) >> 23) - 127;
+                ex = (top == 0.0f || ex == 128) ? 0 : max(-126, min(126, ex));
+                up = __uint_as_float(uint32_t(127 - ex) << 23);
+                down = __uint_as_float(uint32_t(127 + ex) << 23);
+            }
+            row_c[r] = A.sm_scale * kLog2e * down;
+#pragma unroll
+            for (int j = 0; j < kQuads; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float *f = &x[j][4 * k];
+                    qf[4 * j + k][r] = h2(__floats2half2_rn(f[0] * up, f[1] * up));
+                    qf[4 * j + k][2 + r] = h2(__floats2half2_rn(f[2] * up, f[3] * up));
+                }
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+        u_ref = 0.0f;
+    };
+
+    // Writes the open segment's piece.
+    auto close_segment = [&]() {
+        const bool begins = seg_blk == sq.lo;
+        const int64_t seg_end = start + seg_i - (seg_blk - sq.lo) + sq.nb;
+        const bool whole = begins && seg_end <= start + count;
+        const int rows = sq.n * A.G - row0;
+        const int slot = 2 * w + (seg_i == 0 ? 0 : 1);
+        if (begins && !whole) {
+            split = true;
+            if (lane == 0) A.meta[w] = make_int4(seg_b, seg, int((seg_end - 1) / chunk), slot);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            const int rt = g + 8 * r;
+            if (rt >= rows) continue;
+            if (whole) {
+                const float f = l[r] == 0.0f ? 0.0f : u_ref / (kPScale * l[r]);
+                const int rr = row0 + rt, i = rr / A.G, hq = head * A.G + rr - i * A.G;
+                const int64_t at = (int64_t(sq.ts) + i) * (A.H * A.G) + hq;
+                T *dst = static_cast<T *>(A.o) + at * D;
+                if (A.lse && c == 0) A.lse[at] = l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int ch = D == 128 ? 16 * (c + 4 * e) : 16 * c + 8 * e;
+#pragma unroll
+                    for (int i8 = 0; i8 < kNT; i8 += 8) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            p[k] = pack_out(acc[i8 + 2 * k][2 * r + e] * f, acc[i8 + 2 * k + 1][2 * r + e] * f, T());
+                        *reinterpret_cast<uint4 *>(dst + ch + i8) = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                }
+            } else {
+                float *part = A.part + int64_t(slot) * S::kPart;
+                if (c == 0) {
+                    part[kRows * D + rt] = m[r];
+                    part[kRows * D + kRows + rt] = l[r];
+                }
+                const float f = u_ref * (1.0f / kPScale);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int ch = D == 128 ? 16 * (c + 4 * e) : 16 * c + 8 * e;
+#pragma unroll
+                    for (int k = 0; k < kNT; k += 4)
+                        *reinterpret_cast<float4 *>(part + rt * D + ch + k) =
+                            make_float4(acc[k][2 * r + e] * f, acc[k + 1][2 * r + e] * f, acc[k + 2][2 * r + e] * f,
+                                        acc[k + 3][2 * r + e] * f);
+                }
+            }
+        }
+    };
+
+    for (int i = 0; i < count; ++i) {
+        if (i - window == 32) {
+            cur = nxt;
+            window += 32;
+            nxt = next_entry(start + window + 32 + lane);
+        }
+        const int at = i - window;
+        const int b = __shfl_sync(0xffffffffu, cur.b, at), sg = __shfl_sync(0xffffffffu, cur.seg, at);
+        const int blk = __shfl_sync(0xffffffffu, cur.blk, at);
+        const float sk = __shfl_sync(0xffffffffu, cur.sk, at), sv = __shfl_sync(0xffffffffu, cur.sv, at);
+        if (b != seg_b || sg != seg) {
+            if (seg_b >= 0) close_segment();
+            open_segment(b, sg);
+            seg_b = b;
+            seg = sg;
+            seg_i = i;
+            seg_blk = blk;
+        }
+        const int t0 = blk * kPage;
+        const bool seen = t0 <= tile_last && t0 + kPage > tile_first;
+        const bool full = t0 >= all_first && t0 + kPage - 1 <= all_last;
+
+        // ---- S = q . k8
+        ok = mbar_wait(bars + 8 * uint32_t(done % kSlots), uint32_t(done / kSlots) & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        float s[8][4];
+        if (seen) {
+            const uint8_t *tile = ring + (done % kSlots) * S::kTile;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+                const int key = 8 * nt + (D == 128 ? (g & 1) * 4 + (g >> 1) : g);
+#pragma unroll
+                for (int j = 0; j < kQuads; ++j) {
+                    const int chunk16 = D == 128 ? c + 4 * j : (key & 1) * 4 + c;
+                    const int ln = D == 128 ? key : key >> 1;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + ln * 128 + ((chunk16 ^ (ln & 7)) << 4));
+                    const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t u8 = wd[k] ^ 0x80808080u;
+                        mma16816(s[nt], qf[4 * j + k], bytes_to_h2(u8, 0x4140u), bytes_to_h2(u8, 0x4342u));
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        issue(done + kSlots, window);
+        ++done;
+
+        // ---- p = exp(x - m), in powers of two
+        uint32_t pf[8][2];
+        if (seen) {
+            float ratio, su = 1.0f;
+            if (sv > u_ref && sv < INFINITY) {
+                su = u_ref / sv;
+                u_ref = sv;
+                ratio = kPScale;
+            } else {
+                ratio = sv == 0.0f ? 0.0f : kPScale * (sv / u_ref);
+            }
+            float factor[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float sc = row_c[r] * sk;
+                float top = -INFINITY;
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = s[nt][2 * r + e] * sc;
+                        if (!full) {
+                            const int t = t0 + 8 * nt + (D == 128 ? c + 4 * e : 2 * c + e);
+                            if (t < row_first[r] || t > row_last[r]) x = -INFINITY;
+                        }
+                        s[nt][2 * r + e] = x;
+                        top = fmaxf(top, x);
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float m_new = fmaxf(m[r], top);
+                const float ref = m_new == -INFINITY ? 0.0f : m_new;
+                const float alpha = ex2_approx(m[r] - ref);
+                float sum = 0.0f;
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    float p[2], y[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = s[nt][2 * r + e];
+                        p[e] = ex2_approx(x - ref);
+                        y[e] = p[e] * ratio;
+                        if (!full && x == -INFINITY) y[e] = 0.0f;  // whatever the block's scale
+                    }
+                    sum += p[0] + p[1];
+                    pf[nt][r] = h2(__floats2half2_rn(y[0], y[1]));
+                }
+                l[r] = l[r] * alpha + sum;
+                m[r] = m_new;
+                factor[r] = alpha * su;
+            }
+            if (__any_sync(0xffffffffu, factor[0] != 1.0f || factor[1] != 1.0f)) {
+#pragma unroll
+                for (int k = 0; k < kNT; ++k) {
+                    acc[k][0] *= factor[0];
+                    acc[k][1] *= factor[0];
+                    acc[k][2] *= factor[1];
+                    acc[k][3] *= factor[1];
+                }
+            }
+        }
+
+        // ---- acc += p . v8
+        ok = mbar_wait(bars + 8 * uint32_t(done % kSlots), uint32_t(done / kSlots) & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (seen) {
+            const uint8_t *tile = ring + (done % kSlots) * S::kTile;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {  // 16 keys
+                uint32_t vw[4][kNT / 4];      // 4 keys x kNT channels of this lane
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int in8 = D == 128 ? c + 4 * (y & 1) : 2 * c + (y & 1);
+                    const int key = 16 * kk + 8 * (y >> 1) + in8;
+                    if (D == 128) {
+                        const int chunk16 = (g & 1) * 4 + (g >> 1);
+                        const uint4 v =
+                            *reinterpret_cast<const uint4 *>(tile + key * 128 + ((chunk16 ^ (key & 7)) << 4));
+                        vw[y][0] = v.x;
+                        vw[y][1] = v.y;
+                        vw[y][kNT / 4 - 2] = v.z;
+                        vw[y][kNT / 4 - 1] = v.w;
+                    } else {
+                        const int ln = key >> 1, chunk16 = (key & 1) * 4 + (g >> 1);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(
+                            tile + ln * 128 + ((chunk16 ^ (ln & 7)) << 4) + 8 * (g & 1));
+                        vw[y][0] = v.x;
+                        vw[y][1] = v.y;
+                    }
+                }
+                const uint32_t a[4] = {pf[2 * kk][0], pf[2 * kk][1], pf[2 * kk + 1][0], pf[2 * kk + 1][1]};
+#pragma unroll
+                for (int q4 = 0; q4 < kNT / 4; ++q4) {
+                    uint32_t lo[2], hi[2];  // channels 4 q4 + {0, 1}, {2, 3} of both key pairs
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t w0 = vw[2 * y][q4], w1 = vw[2 * y + 1][q4];
+                        lo[y] = __byte_perm(w0, w1, 0x5140) ^ 0x80808080u;
+                        hi[y] = __byte_perm(w0, w1, 0x7362) ^ 0x80808080u;
+                    }
+                    mma16816(acc[4 * q4], a, bytes_to_h2(lo[0], 0x4140u), bytes_to_h2(lo[1], 0x4140u));
+                    mma16816(acc[4 * q4 + 1], a, bytes_to_h2(lo[0], 0x4342u), bytes_to_h2(lo[1], 0x4342u));
+                    mma16816(acc[4 * q4 + 2], a, bytes_to_h2(hi[0], 0x4140u), bytes_to_h2(hi[1], 0x4140u));
+                    mma16816(acc[4 * q4 + 3], a, bytes_to_h2(hi[0], 0x4342u), bytes_to_h2(hi[1], 0x4342u));
+                }
+            }
+        }
+        __syncwarp();
+        issue(done + kSlots, window);
+        ++done;
+    }
+    if (ok) {
+        close_segment();
+    } else {
+        if (lane == 0) record(6);
+        // the tiles still in flight must land before the block's shared memory is given up
+        for (int u = done; u < min(done + kSlots, 2 * count); ++u)
+            for (int i = 0; i < 1 << 20 && !mbar_try_wait(bars + 8 * uint32_t(u % kSlots), uint32_t(u / kSlots) & 1u); ++i) {
+            }
+    }
+    if (!split && lane == 0) A.meta[w] = make_int4(0, 0, 0, 0);
+}
+
+// Joins the pieces of the segment that worker blockIdx.x began and others went on with.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cache_combine_kernel(const CacheAttnArgs A)
+{
+    constexpr int kPart = Sizes<D>::kPart, kPer = D / 32;
+    __shared__ float sums[kWarps][D];
+    const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 meta = A.meta[w];
+    if (meta.z <= w) return;
+    const Seq sq = load_seq(A, meta.x);
+    const int head = meta.y / sq.tiles, row0 = (meta.y - head * sq.tiles) * kRows;
+    const int rows = min(kRows, sq.n * A.G - row0), pieces = meta.z - w + 1;
+    int groups = 1;
+    while (groups < rows && groups < kWarps) groups *= 2;
+    const int subs = kWarps / groups, sub = warp / groups;
+    auto part_of = [&](int p) { return A.part + int64_t(p == 0 ? meta.w : 2 * (w + p)) * kPart; };
+    for (int r0 = 0; r0 < rows; r0 += groups) {
+        const int r = r0 + warp % groups;
+        float big = -INFINITY, total = 0.0f, out[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) out[k] = 0.0f;
+        if (r < rows) {
+            for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[kRows * D + r]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const float ref = big == -INFINITY ? 0.0f : big;
+            for (int p = lane; p < pieces; p += 32) {
+                const float *part = part_of(p);
+                total += ex2_approx(part[kRows * D + r] - ref) * part[kRows * D + kRows + r];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll 4
+            for (int p = sub; p < pieces; p += subs) {
+                const float *part = part_of(p);
+                const float f = ex2_approx(part[kRows * D + r] - ref);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) out[k] += f * part[r * D + lane + 32 * k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) sums[warp][lane + 32 * k] = out[k];
+        __syncthreads();
+        if (sub == 0 && r < rows) {
+            const float f = total == 0.0f ? 0.0f : 1.0f / total;
+            const int rr = row0 + r, i = rr / A.G;
+            const int64_t at = (int64_t(sq.ts) + i) * (A.H * A.G) + head * A.G + rr - i * A.G;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                float x = 0.0f;
+                for (int y = 0; y < subs; ++y) x += sums[warp + y * groups][lane + 32 * k];
+                const uint32_t p = pack_out(x * f, 0.0f, T());
+                static_cast<uint16_t *>(A.o)[at * D + lane + 32 * k] = uint16_t(p);
+            }
+            if (A.lse && lane == 0) A.lse[at] = total == 0.0f ? -INFINITY : (big + log2f(total)) * kLn2;
+        }
+        __syncthreads();
+    }
+}
+
+int workers_of(int sms) { return sms * kWarps; }
+
+template <typename T, int D>
+cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms, cudaStream_t st)
+{
+    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(Sizes<D>::kAlloc));
+    if (e != cudaSuccess) return e;
+    cache_attn_kernel<T, D><<<sms, kThreads, Sizes<D>::kAlloc, st>>>(tm_k, tm_v, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cache_combine_kernel<T, D><<<workers_of(sms), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t sm_count(int *sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
+size_t meta_bytes(int sms) { return (size_t(workers_of(sms)) * sizeof(int4) + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t cache_attn_workspace(int sms, int d)
+{
+    return meta_bytes(sms) + size_t(2) * workers_of(sms) * size_t(d == 128 ? Sizes<128>::kPart : Sizes<64>::kPart) * 4;
+}
+
+cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
+                              cudaStream_t st)
+{
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    a.meta = static_cast<int4 *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + meta_bytes(sms));
+    if (a.dtype == 0)
+        return a.d == 128 ? launch_for<__nv_bfloat16, 128>(tm_k, tm_v, a, sms, st)
+                          : launch_for<__nv_bfloat16, 64>(tm_k, tm_v, a, sms, st);
+    return a.d == 128 ? launch_for<__half, 128>(tm_k, tm_v, a, sms, st) : launch_for<__half, 64>(tm_k, tm_v, a, sms, st);
+}
+
+cudaError_t read_and_clear_cache_attn_status(int *status)
+{
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyFromSymbol(status, g_cache_attn_status, sizeof(int));
+    if (e != cudaSuccess) return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_cache_attn_status, &zero, sizeof(int));
+}
+
+}  // namespace sa

@@ -108,6 +108,58 @@ cudaError_t launch_sla_linear(const void *q, const void *k, const void *v, const
 // keep[e] = classes[e] >= 2 (the sparse part's block mask), n entries.
 cudaError_t launch_sla_critical(const uint8_t *classes, int64_t n, uint8_t *keep, cudaStream_t st);
 cudaError_t read_and_clear_sla_status(int *status);
+// ---- rotary positions (sa_rope.cu)
+struct RopeIo {
+    const void *x = nullptr;
+    void *y = nullptr;
+    int64_t xb = 0, xh = 0, xn = 0, yb = 0, yh = 0, yn = 0;  // strides in elements
+    int heads = 0;
+};
+struct RopeArgs {
+    RopeIo io[2];
+    int B = 1, N = 0, d = 0, rot = 0;
+    int interleaved = 0, inverse = 0;
+    const int32_t *pos = nullptr;
+    int64_t pos_axis_stride = 0, pos_batch_stride = 0;
+    int axis_end[3] = {0, 0, 0};  // pair p turns with axis (p >= end[0]) + (p >= end[1]) + (p >= end[2])
+    const double *freqs = nullptr;
+    float amplitude = 1.0f;
+    int tile_tokens = 0, heads_per_block = 0;  // set by the launcher
+};
+// dtype: 0 bf16, 1 fp16, 2 fp32
+cudaError_t launch_rope(RopeArgs a, int dtype, cudaStream_t st);
+// ---- paged INT8 cache (sa_cache.cu, sa_cache_attn.cu)
+constexpr int kPage = 64;  // tokens of a page
+struct CacheArgs {
+    const void *k = nullptr, *v = nullptr;  // append: the new tokens; read: the destinations
+    int64_t k_stride = 0, v_stride = 0;
+    int8_t *k_codes = nullptr, *v_codes = nullptr;
+    float *k_scale = nullptr, *v_scale = nullptr;
+    const int32_t *tok_start = nullptr, *kv_lens = nullptr, *table = nullptr;
+    int T = 0, B = 0, H = 0, d = 0, max_pages = 0, num_pages = 0;
+};
+cudaError_t launch_cache_append(const CacheArgs &a, int dtype, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheArgs &a, int dtype, cudaStream_t st);
+cudaError_t read_and_clear_cache_status(int *status);
+struct CacheAttnArgs {
+    const void *q = nullptr;
+    void *o = nullptr;
+    float *lse = nullptr;
+    int dtype = 0;
+    int64_t q_stride = 0;
+    const float *k_scale = nullptr, *v_scale = nullptr;
+    const int32_t *tok_start = nullptr, *kv_lens = nullptr, *table = nullptr;
+    int T = 0, B = 0, H = 0, G = 1, d = 0, max_pages = 0, num_pages = 0;  // H key/value heads, G query heads on each
+    int causal = 1, window = 0;
+    float sm_scale = 0.0f;
+    int4 *meta = nullptr;   // set by the launcher, in the workspace
+    float *part = nullptr;
+};
+size_t cache_attn_workspace(int sms, int d);
+// tm_k, tm_v: the codes as 128-byte lines, a box of one head's page, 128-byte swizzle
+cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
+                              cudaStream_t st);
+cudaError_t read_and_clear_cache_attn_status(int *status);
 // Reads and clears the device status word of the current device (synchronous).
 cudaError_t read_and_clear_status(int *status);
 // ---- measured tensor-core peak (sa_peak.cu): one CTA per SM, reps chains of four

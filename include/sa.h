@@ -40,7 +40,9 @@
  *     sa_get_device_status, which synchronises the device.
  *   - Argument errors are detected on the host before any launch; outputs are then
  *     untouched.  Launch failures return SA_ERR_CUDA.  Device-side bounded waits that
- *     expire set a device status word read by sa_get_device_status.
+ *     expire set a device status word read by sa_get_device_status, and so do
+ *     page numbers, lengths and offsets in device memory that are out of range (see the
+ *     cache calls, which skip what they would have reached).
  *   - Block mask: uint8 [B,H,nq,nk], nonzero keeps the (128-query x 64-key) block; NULL
  *     keeps every block.  Masked blocks are neither loaded nor computed.  With a mask,
  *     nk <= 16384 (N <= 1,048,576), else SA_ERR_UNSUPPORTED.
@@ -77,7 +79,8 @@ typedef enum {
     SA_ERR_CUDA = 4,           /* a CUDA runtime/driver call or launch failed */
     SA_ERR_OOM = 5,            /* the library workspace could not be allocated */
     SA_ERR_DEVICE_TIMEOUT = 6, /* a device-side bounded wait expired */
-    SA_ERR_SCRATCH_LIMIT = 7   /* the problem needs more than a fixed scratch array holds */
+    SA_ERR_SCRATCH_LIMIT = 7,  /* the problem needs more than a fixed scratch array holds */
+    SA_ERR_BAD_INDEX = 8       /* a page, length or offset read on the device is out of range */
 } sa_status;
 
 /* Quantise Q and smooth + quantise K (the Q/K half of the prologue).
@@ -271,6 +274,119 @@ sa_status sa_sla_linear(const void *q, const void *k, const void *v, const uint8
 sa_status sa_sla_fwd(const void *q, const void *k, const void *v, void *o, int B, int H, int N, int d,
                      float sm_scale, const uint8_t *classes, int phi, const float *proj, void *stream);
 
+/* ---- Generation over a cache: rotary positions, a paged INT8 key/value cache, attention over it.
+ * Sources: "AIGC weekend special 5.10", sections 4 (HiAR) and 6 (SDVG): causal and
+ * autoregressive video generation, where each new latent frame attends to the frames before
+ * it, whose keys and values are kept; section 1.2 Method item (1): low-bit keys.  The pages
+ * give no cache format and no position code; what is computed is stated here in full.
+ *
+ * Conventions of these calls, beyond those above:
+ *   - dtype is SA_BF16, SA_FP16 or (sa_rope, sa_cache_read) SA_FP32, the type of q, k, v, o.
+ *   - Tokens are packed: T tokens, those of sequence b being tok_start[b] .. tok_start[b + 1] - 1
+ *     (int32 [B + 1], device).  kv_lens[b] (int32 [B], device) counts the cached tokens of
+ *     sequence b INCLUDING these n = tok_start[b + 1] - tok_start[b], which stand at the
+ *     positions kv_lens[b] - n .. kv_lens[b] - 1.  A token whose position is negative is
+ *     padding (kv_lens[b] = 0 for an idle row of a fixed batch): it is not stored, reads as
+ *     zero and attends to nothing.  Tokens before tok_start[0] or from tok_start[B] on belong to no
+ *     sequence: they are not read, and their rows of the outputs are left as they were.
+ *   - page_table int32 [B, max_pages] (device): token t of sequence b is row t % 64 of page
+ *     page_table[b][t / 64].  Entries past a sequence's last page are not read.
+ *   - The cache, device memory of the caller: codes int8 [num_pages, H, 64, d] and scales fp32
+ *     [num_pages, H] (>= 0), for keys and for values; a value is scale * code.  d = 64 or 128.
+ *   - Lengths, offsets and pages are read on the device, so a captured graph follows their
+ *     changes.  One that is out of range (page outside [0, num_pages), length above
+ *     64 * max_pages, offsets that decrease or pass T) sets SA_ERR_BAD_INDEX in the device
+ *     status word: nothing is stored through it, a bad page reads as NaN, and a sequence whose
+ *     length or offsets are bad is left out, its output rows as they were.
+ *   - T = 0 (N = 0) is a valid call that does nothing.
+ *   - The codes, k, v, q, o, x, y and the workspace are 16-byte aligned; freqs 8-byte; the int32
+ *     and the other fp32 arrays 4-byte.  Token strides are in elements, multiples of 16 bytes, and at
+ *     least a token's heads * d; a token's heads follow each other without a gap.  B <= 2^20,
+ *     T <= 2^30, H <= 65535, 64 * max_pages <= 2^30, num_pages * H * d / 2 <= 2^31 - 1.
+ *   - No call uses the library workspace or allocates anything. */
+enum { SA_BF16 = 0, SA_FP16 = 1, SA_FP32 = 2 };
+enum { SA_ROPE_PLAIN = 0, SA_ROPE_LINEAR = 1, SA_ROPE_BASE = 2, SA_ROPE_RAMP = 3 };
+enum { SA_CACHE_PAGE = 64 };
+
+/* Host only: the rotation frequencies (radians per position) freqs double [rot / 2] and the
+ * amplitude of a rotary code of `rot` channels (a multiple of 16):
+ *   SA_ROPE_PLAIN   base^(-2i/rot);
+ *   SA_ROPE_LINEAR  the same divided by factor (positions squeezed);
+ *   SA_ROPE_BASE    with base * factor^(rot/(rot-2)) for base: the fastest pair as it was, the
+ *                   slowest divided by factor;
+ *   SA_ROPE_RAMP    pairs that turn more than beta_fast times within original_len positions as
+ *                   they were, those that turn less than beta_slow times divided by factor, the
+ *                   ones between mixed linearly in the pair's index; amplitude
+ *                   0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023).
+ * base > 1, factor >= 1; original_len >= 1 and beta_fast > beta_slow > 0 for SA_ROPE_RAMP. */
+sa_status sa_rope_frequencies(int rot, double base, int scaling, double factor, int original_len,
+                              double beta_fast, double beta_slow, double *freqs, float *amplitude);
+
+/* One tensor of a rotation: x -> y, [B, heads, N, d] by element strides of batch, head and
+ * token (channels contiguous).  y == x with equal strides rotates in place; x and y must not
+ * overlap in any other way. */
+typedef struct {
+    const void *x;
+    void *y;
+    int64_t x_batch, x_head, x_tok, y_batch, y_head, y_tok;
+    int heads;
+} sa_rope_tensor;
+
+/* Rotary positions of one or two tensors (q, and k if count = 2) that share their tokens, in
+ * one launch.  Pair i of the first `rot` channels of a head -- channels (i, i + rot/2), or
+ * (2i, 2i + 1) if interleaved -- turns by the angle pos * freqs[i] (fp64, freqs device [rot/2])
+ * and is multiplied by amplitude; inverse != 0 turns the other way, which is the transposed
+ * map.  The other channels are copied.  Computed in fp32, rounded once.
+ * pos int32 (device): token n of batch b on axis a is pos[a * pos_axis + b * pos_batch + n];
+ * pair i belongs to axis a where sections[0] + .. + sections[a - 1] <= i; sections (host,
+ * axes <= 4 counts that sum to rot / 2) may be NULL with axes = 1.  pos_batch = 0 shares the
+ * positions among the batches.  d a multiple of 16 up to 256, rot a multiple of 16 up to d. */
+sa_status sa_rope(const sa_rope_tensor *tensors, int count, int dtype, int B, int N, int d, int rot,
+                  int interleaved, const int32_t *pos, int64_t pos_axis, int64_t pos_batch, int axes,
+                  const int *sections, const double *freqs, float amplitude, int inverse, void *stream);
+
+/* Writes the new tokens k, v [T, H, d] (SA_BF16 or SA_FP16, token strides k_tok, v_tok) into
+ * the cache.  For each block of 64 tokens and each head, keys and values apart: s_new =
+ * fl(max|x| / 127) over the block's new tokens; the scale becomes s = s_new for a block without
+ * older tokens, else max(s_old, s_new), the older codes c becoming rint(fl(c * fl(s_old / s)));
+ * the new codes are rint(fl(x / s)) within +-127 (fl: one rounding to fp32; rint: ties to
+ * even; codes 0 where s = 0).  A code that was written at once is off by at most s/2; each
+ * later growth of the block's scale adds at most s/2 of the new scale.  Non-finite values make the block read as NaN.
+ * Sequences must not share a page that this call writes. */
+sa_status sa_cache_append(const void *k, const void *v, int dtype, int64_t T, int64_t k_tok, int64_t v_tok,
+                          const int32_t *tok_start, const int32_t *kv_lens, const int32_t *page_table, int B,
+                          int max_pages, int8_t *k_codes, float *k_scale, int8_t *v_codes, float *v_scale,
+                          int num_pages, int H, int d, void *stream);
+
+/* Reads the values of the tokens at tok_start / kv_lens out of the cache: k, v contiguous
+ * [T, H, d] of dtype (either may be NULL), scale * code rounded once. */
+sa_status sa_cache_read(void *k, void *v, int dtype, int64_t T, const int32_t *tok_start,
+                        const int32_t *kv_lens, const int32_t *page_table, int B, int max_pages,
+                        const int8_t *k_codes, const float *k_scale, const int8_t *v_codes,
+                        const float *v_scale, int num_pages, int H, int d, void *stream);
+
+/* Attention of the T query tokens q [T, H * group, d] (SA_BF16 or SA_FP16, token stride q_tok)
+ * over the cache, whose tokens include the queries' own (append first).  Query head h reads
+ * key/value head h / group.  The query at position p sees the tokens t < kv_lens[b] with
+ * t <= p (causal != 0) and t > p - window (window > 0; 0: no window).
+ *   o [T, H * group, d] (contiguous, dtype) = sum_t softmax_t(q . k_t * sm_scale) v_t, and lse
+ *   fp32 [T, H * group] (or NULL) = log sum_t exp(q . k_t * sm_scale); a query that sees
+ *   nothing has o = 0 and lse = -inf.
+ * Products of fp16 operands (the codes and, up to a power of two for each row, q are exact;
+ * softmax weights are rounded to fp16), sums and statistics in fp32.  The result does not
+ * depend on timing.  workspace: device memory of at least
+ * sa_cache_attn_workspace_bytes(T, B, H, group, d) bytes, which the call may overwrite and which no other call may use meanwhile; it need not
+ * be set before or kept after. */
+sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T, int64_t q_tok,
+                        const int32_t *tok_start, const int32_t *kv_lens, const int32_t *page_table, int B,
+                        int max_pages, const int8_t *k_codes, const float *k_scale, const int8_t *v_codes,
+                        const float *v_scale, int num_pages, int H, int group, int d, int causal, int window,
+                        float sm_scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that sa_cache_attn needs for these sizes on the current device (0: sizes
+ * that it refuses, or no device). */
+size_t sa_cache_attn_workspace_bytes(int64_t T, int B, int H, int group, int d);
+
 /* Debug: the int32 S = q_i8 . k_i8^T tiles computed by the same tcgen05 INT8 path the
  * attention kernel uses, stored to s_out int32 [B,H,Npad,Npad] (padded rows/keys
  * included).  For bit-exact checks on small problems only.  Allocates nothing. */
@@ -284,7 +400,8 @@ sa_status sa_debug_wait_timeout(int timeout_us, void *stream);
 
 
 /* Synchronises the current device, returns and clears its device status word
- * (SA_OK or SA_ERR_DEVICE_TIMEOUT), or SA_ERR_CUDA if synchronisation failed. */
+ * (SA_OK, SA_ERR_DEVICE_TIMEOUT or SA_ERR_BAD_INDEX), or SA_ERR_CUDA if synchronisation
+ * failed. */
 sa_status sa_get_device_status(void);
 
 /* Human-readable name of a status code (static string). */

@@ -1,0 +1,237 @@
+"""Attention over the paged INT8 cache against 64-bit attention over the values it stands for."""
+import math
+
+import pytest
+import torch
+
+from _cache_ref import attn_ref, check_attn, random_cache, random_table, starts_of
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(seed, new, lens, H, G, d, dtype, extra_pages=3, q_scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    pages = sum(-(-n // 64) for n in lens) + extra_pages
+    cache, table = random_cache(gen, pages, H, d), random_table(gen, lens, pages, extra=1)
+    q = (q_scale * torch.randn(sum(new), H * G, d, generator=gen)).cuda().to(dtype)
+    return cache, q, starts_of(new), torch.tensor(lens, dtype=torch.int32, device="cuda"), table
+
+
+def _run(libsa, case, dtype, **kw):
+    cache, q, starts, lens, table = case
+    got = libsa.sa_cache_attn(cache, q, starts, lens, table, return_lse=True, **kw)
+    assert libsa.sa_get_device_status() == 0
+    check_attn(got, attn_ref(cache, q, starts, lens, table, **kw), dtype)
+    return got
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,G", [(1, 1), (3, 5), (2, 16), (1, 17), (2, 40)])
+def test_single_tokens(libsa, cuda_ok, d, dtype, H, G):
+    lens = [1, 2, 63, 64, 65, 128, 700, 3333]
+    _run(libsa, _case(d + G, [1] * len(lens), lens, H, G, d, dtype), dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [0, 1, 64, 200])
+def test_chunks(libsa, cuda_ok, d, causal, window):
+    """Pieces of 2 to 300 tokens, from the first of a sequence to deep in it."""
+    new, lens = [2, 1, 300, 65, 129, 17], [2, 64, 300, 200, 1000, 4099]
+    _run(libsa, _case(d + window, new, lens, 2, 3, d, torch.bfloat16), torch.bfloat16, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("G", [1, 2, 7])
+def test_long_chunks(libsa, cuda_ok, G):
+    new, lens = [700, 513], [2500, 513]
+    _run(libsa, _case(G, new, lens, 2, G, 128, torch.float16), torch.float16)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_rows_that_see_nothing(libsa, cuda_ok, new):
+    """Idle sequences, tokens before their sequence, empty pieces, rows before the first and
+    behind the last sequence: zero and -inf, or left as they were."""
+    d, H, G = 128, 2, 2
+    news, lens = [new, new, 0, new, new], [0, 130, 64, max(0, new - 3), 0]
+    cache, q, starts, dlens, table = _case(7, news, [max(n, 1) for n in lens], H, G, d, torch.bfloat16)
+    dlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    check_attn(libsa.sa_cache_attn(cache, q, starts, dlens, table, return_lse=True),
+               attn_ref(cache, q, starts, dlens, table), torch.bfloat16)
+    wide = torch.cat([q[:3], q, torch.cat([q, q])[:5]])  # 3 rows before, 5 behind
+    out = torch.full((wide.shape[0], H * G, d), 9.0, device="cuda", dtype=torch.bfloat16)
+    libsa.sa_cache_attn(cache, wide, starts + 3, dlens, table, out=out)
+    assert (out[:3] == 9).all() and (out[-5:] == 9).all()
+    assert torch.equal(out[3:-5], libsa.sa_cache_attn(cache, q, starts, dlens, table))
+    assert libsa.sa_get_device_status() == 0
+
+
+def test_no_attention_outside_a_sequence_even_to_nan(libsa, cuda_ok):
+    """Stale rows of a last page, and blocks that a row does not see, may hold anything: a NaN
+    scale reaches only the rows that see its block."""
+    d, H, G = 128, 1, 2
+    for new in (1, 100):
+        cache, q, starts, lens, table = _case(21, [new], [320], H, G, d, torch.bfloat16)
+        clean = libsa.sa_cache_attn(cache, q, starts, lens, table, window=100)
+        for bad in (math.nan, math.inf):
+            ks, vs = cache[1].clone(), cache[3].clone()
+            first = table[0, 0].long()
+            ks[first], vs[first] = bad, bad                    # out of every window
+            other = [p for p in range(cache[0].shape[0]) if p not in table[0, :5].tolist()]
+            ks[other], vs[other] = math.nan, math.nan          # pages of nobody
+            got = libsa.sa_cache_attn((cache[0], ks, cache[2], vs), q, starts, lens, table, window=100)
+            assert torch.equal(got, clean)
+            vs[table[0, 4].long()] = bad                       # the last block: rows at 256 and on see it
+            got = libsa.sa_cache_attn((cache[0], ks, cache[2], vs), q, starts, lens, table, window=100)
+            sees = torch.arange(320 - new, 320, device="cuda") >= 256
+            assert not torch.isfinite(got[sees].float()).any()
+            assert torch.equal(got[~sees], clean[~sees])
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 30.0, 1e30])
+def test_query_range(libsa, cuda_ok, scale):
+    """bf16 queries far outside fp16's range, with the logit scale that brings scores back."""
+    case = _case(31, [1, 40], [500, 333], 2, 3, 128, torch.bfloat16, q_scale=scale)
+    _run(libsa, case, torch.bfloat16, sm_scale=0.09 / scale)
+
+
+def test_value_scales_of_many_sizes(libsa, cuda_ok):
+    """Blocks whose value scales differ by 2^30, zero ones among them, and zero key scales."""
+    for new in (1, 70):
+        cache, q, starts, lens, table = _case(41, [new, new], [1500, 800], 2, 4, 64, torch.float16)
+        vs = cache[3] * torch.logspace(-9, 0, cache[3].shape[0], device="cuda")[torch.randperm(cache[3].shape[0])][:, None]
+        vs[::5], ks = 0.0, cache[1].clone()
+        ks[::3] = 0.0
+        _run(libsa, ((cache[0], ks, cache[2], vs), q, starts, lens, table), torch.float16)
+        zero = (cache[0], ks, cache[2], torch.zeros_like(vs))
+        assert (libsa.sa_cache_attn(zero, q, starts, lens, table) == 0).all()
+
+
+def test_sharp_softmax(libsa, cuda_ok):
+    """Scores of several hundred: one key takes a row, and maxima rise along the cache."""
+    _run(libsa, _case(51, [1, 64, 1], [3000, 300, 64], 1, 4, 128, torch.bfloat16, q_scale=20.0), torch.bfloat16)
+
+
+def test_many_sequences_and_few_blocks(libsa, cuda_ok):
+    gen = torch.Generator().manual_seed(61)
+    lens = [int(n) for n in torch.randint(1, 200, (600,), generator=gen)]
+    _run(libsa, _case(62, [1] * 600, lens, 1, 2, 64, torch.bfloat16), torch.bfloat16)
+
+
+def test_one_long_sequence(libsa, cuda_ok):
+    _run(libsa, _case(71, [1], [70001], 2, 4, 128, torch.bfloat16), torch.bfloat16)
+    _run(libsa, _case(72, [1, 1], [40000, 5], 1, 16, 64, torch.float16), torch.float16, window=30000)
+
+
+def test_strided_queries_of_a_fused_projection(libsa, cuda_ok):
+    cache, _, starts, lens, table = _case(81, [1, 1, 1], [100, 200, 64], 2, 2, 128, torch.bfloat16)
+    qkv = torch.randn(3, 8, 128, device="cuda").bfloat16()
+    q = qkv[:, :4]
+    assert not q.is_contiguous()
+    assert torch.equal(libsa.sa_cache_attn(cache, q, starts, lens, table),
+                       libsa.sa_cache_attn(cache, q.contiguous(), starts, lens, table))
+
+
+def test_bad_indexes_are_reported(libsa, cuda_ok):
+    for new in (1, 80):
+        cache, q, starts, lens, table = _case(91, [new, new], [200, 150], 2, 2, 64, torch.bfloat16)
+        good = libsa.sa_cache_attn(cache, q, starts, lens, table)
+        bad = table.clone()
+        bad[0, 1] = cache[0].shape[0]
+        out = libsa.sa_cache_attn(cache, q, starts, lens, bad, causal=False)
+        assert libsa.sa_get_device_status() == 8
+        assert torch.isnan(out[:new]).all() and not torch.isnan(out[new:]).any()
+        long = lens.clone()
+        long[1] = 64 * table.shape[1] + 1
+        out = torch.full_like(q, 5.0)
+        libsa.sa_cache_attn(cache, q, starts, long, table, out=out)
+        assert libsa.sa_get_device_status() == 8
+        assert torch.equal(out[:new], good[:new]) and (out[new:] == 5).all()
+        assert libsa.sa_get_device_status() == 0
+
+
+def _step(libsa, cache, qkv, pos, starts, lens, table, freqs, H, G):
+    """What a decoding layer does: rotate, store, attend."""
+    q, k, v = qkv.split([H * G, H, H], 1)
+    q, k = libsa.sa_rope(q, k, pos, freqs)
+    libsa.sa_cache_append(cache, k, v, starts, lens, table)
+    return libsa.sa_cache_attn(cache, q, starts, lens, table)
+
+
+def test_prompt_then_tokens_as_one_prompt(libsa, cuda_ok):
+    """A prompt in two pieces and twelve single tokens give, row by row, attention over the
+    cache as it stood; a row that ends a block sees the same codes as in one go."""
+    H, G, d, B = 2, 2, 128, 3
+    gen = torch.Generator().manual_seed(101)
+    freqs, _ = libsa.sa_rope_frequencies(d)
+    total = [77, 130, 64]
+    table = random_table(gen, [n + 64 for n in total], 20)
+    cache = libsa.sa_cache_alloc(20, H, d)
+    done = [0] * B
+    for piece in [[40, 100, 1], [25, 18, 51]] + [[1] * B] * 12:
+        done = [a + n for a, n in zip(done, piece)]
+        qkv = torch.randn(sum(piece), H * (G + 2), d, generator=gen).cuda().bfloat16()
+        pos = torch.cat([torch.arange(a - n, a) for a, n in zip(done, piece)]).to(torch.int32).cuda()
+        lens = torch.tensor(done, dtype=torch.int32, device="cuda")
+        o = _step(libsa, cache, qkv, pos, starts_of(piece), lens, table, freqs, H, G)
+        q = libsa.sa_rope(qkv[:, :H * G], None, pos, freqs)
+        check_attn((o, None), attn_ref(cache, q, starts_of(piece), lens, table), torch.bfloat16)
+    assert done == total and libsa.sa_get_device_status() == 0
+
+
+def test_captured_steps_follow_lengths(libsa, cuda_ok):
+    """A captured step, replayed as lengths grow (an idle row among them), equals eager steps;
+    two graphs and eager calls in between do not disturb each other."""
+    H, G, d, B = 2, 3, 64, 4
+    gen = torch.Generator().manual_seed(111)
+    freqs, _ = libsa.sa_rope_frequencies(d)
+    table = random_table(gen, [300] * B, 24)
+    starts = starts_of([1] * B)
+    cache = [libsa.sa_cache_alloc(24, H, d) for _ in range(3)]
+    qkv = torch.zeros(B, H * (G + 2), d, device="cuda", dtype=torch.bfloat16)
+    lens, pos = torch.tensor([62, 127, 0, 200], dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    graphs, outs = [], []
+    for i in range(2):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            _step(libsa, libsa.sa_cache_alloc(24, H, d), qkv, pos, starts, lens, table, freqs, H, G)
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(_step(libsa, cache[i], qkv, pos, starts, lens, table, freqs, H, G))
+        graphs.append(g)
+    for _ in range(70):
+        qkv.copy_(torch.randn(qkv.shape, generator=gen))
+        lens += torch.tensor([1, 1, 0, 1], dtype=torch.int32, device="cuda")
+        pos.copy_((lens - 1).clamp(min=0))
+        graphs[0].replay()
+        want = _step(libsa, cache[2], qkv, pos, starts, lens, table, freqs, H, G)
+        graphs[1].replay()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+        assert (want[2] == 0).all()
+    assert libsa.sa_get_device_status() == 0
+
+
+def test_two_streams_at_once(libsa, cuda_ok):
+    """Calls in flight on two streams have workspaces of their own."""
+    cases = [_case(121 + i, [1] * 8, [5000 + 100 * i] * 8, 4, 4, 128, torch.bfloat16) for i in range(2)]
+    want = [libsa.sa_cache_attn(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        got = []
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(libsa.sa_cache_attn(*c))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
+def test_the_same_call_twice_is_the_same(libsa, cuda_ok):
+    case = _case(131, [1, 1, 50], [9000, 100, 3000], 3, 4, 128, torch.bfloat16)
+    want = libsa.sa_cache_attn(*case, return_lse=True)
+    for _ in range(10):
+        for g, w in zip(libsa.sa_cache_attn(*case, return_lse=True), want):
+            assert torch.equal(g, w)
