@@ -1054,6 +1054,8 @@ sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T
     a.lse = lse;
     a.dtype = dtype;
     a.q_stride = q_tok;
+    a.k_codes = k_codes;
+    a.v_codes = v_codes;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.tok_start = tok_start;
@@ -1119,14 +1121,16 @@ sa_status sa_debug_mma_peak(int kind, int reps, void *stream)
 
 sa_status sa_get_device_status(void)
 {
-    int st = 0, st_w8a8 = 0, st_peak = 0, st_sla = 0, st_cache = 0, st_cattn = 0;
+    int st = 0, st_w8a8 = 0, st_peak = 0, st_sla = 0, st_cache = 0, st_cattn = 0, st_chunk = 0;
     if (read_and_clear_cache_status(&st_cache) != cudaSuccess || read_and_clear_cache_attn_status(&st_cattn) != cudaSuccess ||
+        read_and_clear_cache_chunk_status(&st_chunk) != cudaSuccess ||
         read_and_clear_status(&st) != cudaSuccess || read_and_clear_w8a8_status(&st_w8a8) != cudaSuccess ||
         read_and_clear_peak_status(&st_peak) != cudaSuccess || read_and_clear_sla_status(&st_sla) != cudaSuccess)
         return SA_ERR_CUDA;
-    if (st != 0 || st_w8a8 != 0 || st_peak != 0 || st_sla != 0 || st_cattn == SA_ERR_DEVICE_TIMEOUT)
+    if (st != 0 || st_w8a8 != 0 || st_peak != 0 || st_sla != 0 || st_cattn == SA_ERR_DEVICE_TIMEOUT ||
+        st_chunk == SA_ERR_DEVICE_TIMEOUT)
         return SA_ERR_DEVICE_TIMEOUT;
-    return st_cache == 0 && st_cattn == 0 ? SA_OK : SA_ERR_BAD_INDEX;
+    return st_cache == 0 && st_cattn == 0 && st_chunk == 0 ? SA_OK : SA_ERR_BAD_INDEX;
 }
 
 const char *sa_status_string(sa_status s)

@@ -8,9 +8,9 @@
 //
 // The codes are exact in fp16, and so is q after a power of two for each row (its exponent goes
 // into the row's score scale), so S has no rounding before its fp32 accumulator.  p times the
-// ratio of scale_v[j] to the largest scale_v so far (u) is rounded to fp16, 2^15 times itself:
-// at most 2^15, relative error 2^-12, and what is below 2^-29 of the row's largest weight falls
-// to fp16's subnormals.  acc is kept in units of u * 2^-15.
+// ratio of scale_v[j] to u, the power of two below the largest scale_v so far, is rounded to
+// fp16, 2^14 times itself: at most 2^15, relative error 2^-11, and what is below 2^-28 of the
+// row's largest weight falls to fp16's subnormals.  acc is kept in units of u * 2^-14.
 //
 // What bounds it: reading 2 d bytes for each cached token and head.  So every warp is a worker
 // of its own with a ring of TMA tiles in shared memory (K and V of a block are 64 x d bytes
@@ -23,10 +23,12 @@
 // c ^ (r & 7)), which makes the 16-byte reads below free of bank conflicts at d = 128: the
 // contraction index of an mma may be permuted freely as long as both operands agree, and so
 // may the keys of a tile (scores and values) and the channels (columns of acc).
+#include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "sa_cache_attn.cuh"
 #include "sa_internal.h"
 #include "sa_ptx.cuh"
 
@@ -39,10 +41,11 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;         // rows of a tile
+// Rows of a sequence and head, on average, up to which this kernel takes a call; the others go
+// to the tensor-core kernel of sa_cache_chunk.cu.
+constexpr int kFewRows = 32;
 constexpr int kSlots = 3;         // ring slots of a warp, one K or V tile each
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kPScale = 32768.0f;
+constexpr float kPScale = 16384.0f;
 
 template <int D>
 struct Sizes {
@@ -67,28 +70,11 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const CacheAttnArgs &A, int b)
 {
     Seq s;
-    s.ts = A.tok_start[b];
-    const int te = A.tok_start[b + 1];
-    s.len = A.kv_lens[b];
-    s.n = te - s.ts;
-    if (s.ts < 0 || te < s.ts || te > A.T || s.len < 0 || s.len > int64_t(A.max_pages) * kPage) {
-        record(8);
-        s.n = s.len = s.ts = 0;
-    }
+    if (!load_span(A, b, s.ts, s.n, s.len)) record(8);
     s.tiles = (s.n * A.G + kRows - 1) / kRows;
     s.lo = A.window > 0 ? max(0, s.len - s.n - A.window + 1) / kPage : 0;
     s.nb = max(1, (s.len + kPage - 1) / kPage - s.lo);
     return s;
-}
-
-__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
-
-// two of four bytes u = code + 128 to fp16: 0x6400 + u is 1024 + u, less 1152 is the code
-__device__ __forceinline__ uint32_t bytes_to_h2(uint32_t u, uint32_t sel)
-{
-    const uint32_t p = __byte_perm(u, 0x64646464u, sel);
-    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    return h2(__hsub2(*reinterpret_cast<const __half2 *>(&p), bias));
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -96,34 +82,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_out(float a, float b, __nv_bfloat16)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t pack_out(float a, float b, __half)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// four consecutive values of a row as floats
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&f)[4])
-{
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load4(const __half *p, float (&f)[4])
-{
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
 // One block of the flattened work, held by one lane of a worker's window of 32.
@@ -247,6 +205,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     for (int u = 0; u < kSlots; ++u) issue(u, 0);
 
+    // The reads of a tile are over before TMA writes its slot again: without the proxy fence a read
+    // still in flight can be overtaken.
+    auto release = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+
     bool ok = true;
     int window = 0, done = 0;         // first block of `cur`, tiles consumed
     int seg_b = -1, seg = -1;         // the open segment
@@ -291,16 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top = fmaxf(top, fabsf(f[e]));
                     }
                 }
-            // bf16 has more range than fp16: each row is brought to [1, 4) by a power of two,
-            // exactly; what leaves fp16's normal range then is below 2^-14 of the row's largest
             float up = 1.0f, down = 1.0f;
-            if (sizeof(T) == 2 && A.dtype == 0) {
+            if (A.dtype == 0) {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                int ex = int(__float_as_uint(top) >> 23) - 127;
-                ex = (top == 0.0f || ex == 128) ? 0 : max(-126, min(126, ex));
-                up = __uint_as_float(uint32_t(127 - ex) << 23);
-                down = __uint_as_float(uint32_t(127 + ex) << 23);
+                row_power(top, up, down);
             }
             row_c[r] = A.sm_scale * kLog2e * down;
 #pragma unroll
@@ -420,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        __syncwarp();
+        release();
         issue(done + kSlots, window);
         ++done;
 
@@ -428,13 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pf[8][2];
         if (seen) {
             float ratio, su = 1.0f;
-            if (sv > u_ref && sv < INFINITY) {
-                su = u_ref / sv;
-                u_ref = sv;
-                ratio = kPScale;
-            } else {
-                ratio = sv == 0.0f ? 0.0f : kPScale * (sv / u_ref);
+            if (sv >= 2.0f * u_ref && sv > 0.0f && sv < INFINITY) {
+                const float u_new = scale_ref(sv);
+                su = u_ref / u_new;
+                u_ref = u_new;
             }
+            ratio = sv == 0.0f ? 0.0f : kPScale * (sv / u_ref);
             float factor[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -531,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        __syncwarp();
+        release();
         issue(done + kSlots, window);
         ++done;
     }
@@ -547,44 +506,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!split && lane == 0) A.meta[w] = make_int4(0, 0, 0, 0);
 }
 
-// Joins the pieces of the segment that worker blockIdx.x began and others went on with.
-template <typename T, int D>
+// Joins the pieces of the segment, of ROWS rows at most, that worker blockIdx.x began and others
+// went on with, 16 rows (blockIdx.y) a block.  A piece is acc [ROWS][D], m [ROWS], l [ROWS].
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) cache_combine_kernel(const CacheAttnArgs A)
 {
-    constexpr int kPart = Sizes<D>::kPart, kPer = D / 32;
+    constexpr int kPart = ROWS * (D + 2), kPer = D / 32;
     __shared__ float sums[kWarps][D];
     const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 meta = A.meta[w];
     if (meta.z <= w) return;
-    const Seq sq = load_seq(A, meta.x);
-    const int head = meta.y / sq.tiles, row0 = (meta.y - head * sq.tiles) * kRows;
-    const int rows = min(kRows, sq.n * A.G - row0), pieces = meta.z - w + 1;
+    int ts, n, len;
+    if (!load_span(A, meta.x, ts, n, len)) return;
+    const int tiles = (n * A.G + ROWS - 1) / ROWS;
+    const int head = meta.y / tiles, row0 = (meta.y - head * tiles) * ROWS + 16 * int(blockIdx.y);
+    const int rows = min(16, n * A.G - row0), pieces = meta.z - w + 1;
+    if (rows <= 0) return;
     int groups = 1;
     while (groups < rows && groups < kWarps) groups *= 2;
     const int subs = kWarps / groups, sub = warp / groups;
     auto part_of = [&](int p) { return A.part + int64_t(p == 0 ? meta.w : 2 * (w + p)) * kPart; };
     for (int r0 = 0; r0 < rows; r0 += groups) {
-        const int r = r0 + warp % groups;
+        const int r = r0 + warp % groups, rp = r + 16 * int(blockIdx.y);
         float big = -INFINITY, total = 0.0f, out[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) out[k] = 0.0f;
         if (r < rows) {
-            for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[kRows * D + r]);
+            for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + rp]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             const float ref = big == -INFINITY ? 0.0f : big;
             for (int p = lane; p < pieces; p += 32) {
                 const float *part = part_of(p);
-                total += ex2_approx(part[kRows * D + r] - ref) * part[kRows * D + kRows + r];
+                total += ex2_approx(part[ROWS * D + rp] - ref) * part[ROWS * (D + 1) + rp];
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
 #pragma unroll 4
             for (int p = sub; p < pieces; p += subs) {
                 const float *part = part_of(p);
-                const float f = ex2_approx(part[kRows * D + r] - ref);
+                const float f = ex2_approx(part[ROWS * D + rp] - ref);
 #pragma unroll
-                for (int k = 0; k < kPer; ++k) out[k] += f * part[r * D + lane + 32 * k];
+                for (int k = 0; k < kPer; ++k) out[k] += f * part[rp * D + lane + 32 * k];
             }
         }
 #pragma unroll
@@ -593,7 +556,7 @@ __global__ void __launch_bounds__(kThreads) cache_combine_kernel(const CacheAttn
         if (sub == 0 && r < rows) {
             const float f = total == 0.0f ? 0.0f : 1.0f / total;
             const int rr = row0 + r, i = rr / A.G;
-            const int64_t at = (int64_t(sq.ts) + i) * (A.H * A.G) + head * A.G + rr - i * A.G;
+            const int64_t at = (int64_t(ts) + i) * (A.H * A.G) + head * A.G + rr - i * A.G;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 float x = 0.0f;
@@ -617,7 +580,7 @@ cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const C
     if (e != cudaSuccess) return e;
     cache_attn_kernel<T, D><<<sms, kThreads, Sizes<D>::kAlloc, st>>>(tm_k, tm_v, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cache_combine_kernel<T, D><<<workers_of(sms), kThreads, 0, st>>>(a);
+    cache_combine_kernel<T, D, kRows><<<workers_of(sms), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -634,7 +597,8 @@ size_t meta_bytes(int sms) { return (size_t(workers_of(sms)) * sizeof(int4) + 25
 
 size_t cache_attn_workspace(int sms, int d)
 {
-    return meta_bytes(sms) + size_t(2) * workers_of(sms) * size_t(d == 128 ? Sizes<128>::kPart : Sizes<64>::kPart) * 4;
+    const size_t few = size_t(2) * workers_of(sms) * size_t(d == 128 ? Sizes<128>::kPart : Sizes<64>::kPart) * 4;
+    return meta_bytes(sms) + std::max(few, cache_chunk_part_bytes(sms, d));
 }
 
 cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
@@ -645,6 +609,19 @@ cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, 
     if (e != cudaSuccess) return e;
     a.meta = static_cast<int4 *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + meta_bytes(sms));
+    if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) {
+        if ((e = launch_cache_chunk(tm_k, tm_v, a, sms, st)) != cudaSuccess) return e;
+        const dim3 grid(unsigned(sms), 16);
+        if (a.dtype == 0 && a.d == 128)
+            cache_combine_kernel<__nv_bfloat16, 128, 256><<<grid, kThreads, 0, st>>>(a);
+        else if (a.dtype == 0)
+            cache_combine_kernel<__nv_bfloat16, 64, 256><<<grid, kThreads, 0, st>>>(a);
+        else if (a.d == 128)
+            cache_combine_kernel<__half, 128, 256><<<grid, kThreads, 0, st>>>(a);
+        else
+            cache_combine_kernel<__half, 64, 256><<<grid, kThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
     if (a.dtype == 0)
         return a.d == 128 ? launch_for<__nv_bfloat16, 128>(tm_k, tm_v, a, sms, st)
                           : launch_for<__nv_bfloat16, 64>(tm_k, tm_v, a, sms, st);

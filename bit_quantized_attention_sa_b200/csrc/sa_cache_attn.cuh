@@ -1,0 +1,86 @@
+// sa_cache_attn.cuh -- what the two attention kernels over the paged INT8 cache share: codes to
+// fp16, query rows to fp16, the sequences' arrays, outputs.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sa_internal.h"
+
+namespace sa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+
+// two of four bytes u = code + 128 to fp16: 0x6400 + u is 1024 + u, less 1152 is the code
+__device__ __forceinline__ uint32_t bytes_to_h2(uint32_t u, uint32_t sel)
+{
+    const uint32_t p = __byte_perm(u, 0x64646464u, sel);
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    return h2(__hsub2(*reinterpret_cast<const __half2 *>(&p), bias));
+}
+
+__device__ __forceinline__ uint32_t pack_out(float a, float b, __nv_bfloat16)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_out(float a, float b, __half)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// four consecutive values of a row as floats
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&f)[4])
+{
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const __half *p, float (&f)[4])
+{
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+
+// First token, tokens and cached length of sequence b; false (and an empty sequence) if they
+// are out of range.
+__device__ __forceinline__ bool load_span(const CacheAttnArgs &A, int b, int &ts, int &n, int &len)
+{
+    ts = A.tok_start[b];
+    const int te = A.tok_start[b + 1];
+    len = A.kv_lens[b];
+    n = te - ts;
+    if (ts >= 0 && te >= ts && te <= A.T && len >= 0 && len <= int64_t(A.max_pages) * kPage) return true;
+    ts = n = len = 0;
+    return false;
+}
+
+// The reference that value scales are taken relative to: the power of two at or below x > 0 (a
+// power of two, so that the rounding of a weight does not depend on the scales of blocks that
+// its row does not see).
+__device__ __forceinline__ float scale_ref(float x)
+{
+    return fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 1.17549435e-38f);
+}
+
+// The power of two, and its inverse, that brings a row whose largest magnitude is `top` to
+// [1, 4): bf16 has more range than fp16.  Values that leave fp16's normal range then are below
+// 2^-14 of the row's largest; all others stay exact.
+__device__ __forceinline__ void row_power(float top, float &up, float &down)
+{
+    int ex = int(__float_as_uint(top) >> 23) - 127;
+    ex = (top == 0.0f || ex == 128) ? 0 : max(-126, min(126, ex));
+    up = __uint_as_float(uint32_t(127 - ex) << 23);
+    down = __uint_as_float(uint32_t(127 + ex) << 23);
+}
+
+}  // namespace sa

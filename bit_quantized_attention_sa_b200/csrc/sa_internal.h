@@ -147,6 +147,7 @@ struct CacheAttnArgs {
     float *lse = nullptr;
     int dtype = 0;
     int64_t q_stride = 0;
+    const int8_t *k_codes = nullptr, *v_codes = nullptr;
     const float *k_scale = nullptr, *v_scale = nullptr;
     const int32_t *tok_start = nullptr, *kv_lens = nullptr, *table = nullptr;
     int T = 0, B = 0, H = 0, G = 1, d = 0, max_pages = 0, num_pages = 0;  // H key/value heads, G query heads on each
@@ -160,6 +161,13 @@ size_t cache_attn_workspace(int sms, int d);
 cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
                               cudaStream_t st);
 cudaError_t read_and_clear_cache_attn_status(int *status);
+// The tensor-core kernel for many rows (sa_cache_chunk.cu), called by launch_cache_attn, which
+// joins split segments afterwards.
+constexpr int kCacheChunkMaxSeqs = 4096;
+size_t cache_chunk_part_bytes(int sms, int d);
+cudaError_t launch_cache_chunk(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms,
+                               cudaStream_t st);
+cudaError_t read_and_clear_cache_chunk_status(int *status);
 // Reads and clears the device status word of the current device (synchronous).
 cudaError_t read_and_clear_status(int *status);
 // ---- measured tensor-core peak (sa_peak.cu): one CTA per SM, reps chains of four

@@ -213,6 +213,29 @@ __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t adesc, uint64
         : "memory");
 }
 
+// D(tmem) (+)= A * B^T, fp16 operands, fp32 accumulator; A in shared memory, or in tensor
+// memory (two consecutive values along K in each 32-bit column).
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Instruction descriptor fields (dense, no negation, both operands K-major):
 //   [4,6) accumulator format (1 = f32, 2 = s32); [7,10) A format; [10,13) B format;
 //   [17,23) N >> 3; [24,29) M >> 4.
@@ -233,6 +256,12 @@ __host__ __device__ constexpr uint32_t idesc_tf32_f32(int M, int N, bool a_mn, b
 {
     return (1u << 4) | (2u << 7) | (2u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
            (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// kind::f16 with fp16 operands (format 0), fp32 accumulator; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn)
+{
+    return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
 // Shared-memory matrix descriptor for a K-major operand in a swizzled layout:
@@ -266,6 +295,20 @@ __device__ __forceinline__ uint64_t sdesc_mn32(uint32_t saddr, uint32_t lbo_byte
     d |= uint64_t((sbo_bytes >> 4) & 0x3FFFu) << 32;
     d |= uint64_t(1) << 46;
     d |= uint64_t(SWZ_128B_BASE32B) << 61;
+    return d;
+}
+
+// Descriptor of an MN-major 16-bit operand in the 128-byte swizzle: an atom is 8 rows along K
+// of 128 bytes (64 values) along N; atoms follow each other along N at lbo_bytes and along K
+// at sbo_bytes.
+__device__ __forceinline__ uint64_t sdesc_mn16(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes)
+{
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3FFFu);
+    d |= uint64_t((lbo_bytes >> 4) & 0x3FFFu) << 16;
+    d |= uint64_t((sbo_bytes >> 4) & 0x3FFFu) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(SWZ_128B) << 61;
     return d;
 }
 
