@@ -610,7 +610,7 @@ cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, 
     a.meta = static_cast<int4 *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + meta_bytes(sms));
     if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) {
-        if ((e = launch_cache_chunk(tm_k, tm_v, a, sms, st)) != cudaSuccess) return e;
+        if ((e = launch_cache_chunk(a, sms, st)) != cudaSuccess) return e;
         const dim3 grid(unsigned(sms), 16);
         if (a.dtype == 0 && a.d == 128)
             cache_combine_kernel<__nv_bfloat16, 128, 256><<<grid, kThreads, 0, st>>>(a);

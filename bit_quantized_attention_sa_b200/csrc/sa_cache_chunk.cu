@@ -11,10 +11,10 @@
 // writing of the fp16 tiles), so all three have to run at once:
 //   * warps 0-3 and 4-7: softmax of tile A and B, a thread owning a row (its 128 scores of a step
 //     in registers): maximum, exponentials, P to tensor memory, rescaling of acc, epilogue;
-//   * warps 8-11: the codes of a block, brought by TMA (warp 14, a ring of four 64-token tiles),
-//     become fp16 tiles in shared memory (a ring of four, K and V in turn) in the 128-byte
-//     swizzle that the tensor core reads: K as a K-major operand, V, whose channels are
-//     contiguous, as an MN-major one;
+//   * warps 8-11: the codes, copied ahead from the pages (cp.async, each thread its own 16-byte
+//     parts), become fp16 tiles in shared memory (a ring of four, K and V in turn) in the 128-byte swizzle that
+//     the tensor core reads: K as a K-major operand, V, whose channels are contiguous, as an
+//     MN-major one;
 //   * warp 12 issues S, warp 13 P . V.
 // P is the A operand from tensor memory, which halves P . V's reading of shared memory.  S has
 // one buffer for both tiles in turn, which staggers the two softmax groups by half a step.
@@ -42,22 +42,22 @@ __device__ int g_cache_chunk_status;  // 0 = OK, 6 = a bounded wait expired, 8 =
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kWarpConvert = 8, kWarpQK = 12, kWarpPV = 13, kWarpLoad = 14;
+constexpr int kWarpConvert = 8, kWarpQK = 12, kWarpPV = 13;
 constexpr int kStages = 4;  // fp16 tiles
-constexpr int kRaw = 4;     // 64-token tiles of codes
+constexpr int kRaw = 3;     // half tiles (64 tokens) of codes on their way
 constexpr int kRowsSeg = 256;
 constexpr uint32_t kTmemCols = 512, kColS = 0;
 __host__ __device__ constexpr uint32_t col_p(int t) { return 128u + 64u * uint32_t(t); }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * uint32_t(t); }
-constexpr uint32_t kRegsSoftmax = 208, kRegsConvert = 56, kRegsIssue = 40, kLaunchRegs = 128;
+constexpr uint32_t kRegsSoftmax = 176, kRegsConvert = 112, kRegsIssue = 48, kLaunchRegs = 128;
 static_assert(128 * (2 * kRegsSoftmax + kRegsConvert + kRegsIssue) <= kLaunchRegs * kThreads,
               "the register split must fit the registers the block is launched with");
 constexpr float kGrow = 8.0f;
+constexpr uint32_t kMinusInf = 0xff800000u;
 
 constexpr int kBarQFull = 0, kBarKvFull = 2, kBarKvEmpty = kBarKvFull + kStages, kBarSFull = kBarKvEmpty + kStages,
               kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 1, kBarPvDone = kBarPFull + 2,
-              kBarOFull = kBarPvDone + 2, kBarOEmpty = kBarOFull + 2, kBarRawFull = kBarOEmpty + 2,
-              kBarRawEmpty = kBarRawFull + kRaw, kNumBars = kBarRawEmpty + kRaw;
+              kBarOFull = kBarPvDone + 2, kBarOEmpty = kBarOFull + 2, kNumBars = kBarOEmpty + 2;
 
 template <int D>
 struct Sizes {
@@ -68,8 +68,8 @@ struct Sizes {
     static constexpr uint32_t kRawBytes = 64 * D;
     static constexpr uint32_t kOffRaw = kOffKv + kStages * kTileBytes;
     static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
-    static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
-    static constexpr uint32_t kAlloc = kOffMisc + 16 + 1024;
+    static constexpr uint32_t kOffScale = (kOffBar + 8 * kNumBars + 15) & ~15u;  // of 8 warps, 32 blocks
+    static constexpr uint32_t kAlloc = kOffScale + 8 * 32 * 16 + 1024;
     static constexpr int kPart = kRowsSeg * (D + 2);
 };
 static_assert(Sizes<128>::kAlloc <= 227 * 1024 - 1200, "shared memory per CTA");
@@ -186,6 +186,31 @@ __device__ __forceinline__ void regs_ready(uint32_t (&r)[32])
                  : "memory");
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// 16 codes to shared memory, or zeros; a thread waits for its own copies, group by group.
+__device__ __forceinline__ void copy_codes(uint32_t dst, const int8_t *src, bool any)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(any ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float fl_of(uint32_t x) { return __uint_as_float(x); }
 
 __device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (&b)[32])
@@ -208,32 +233,90 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b)
     return r;
 }
 
-// 32 scores -> 16 words of P; returns the sum of 2^(s * c + bias).
-__device__ __forceinline__ float p32(const uint32_t (&s)[32], float c, float bias, uint32_t *pw)
+// Packed pairs of floats, and in-order forms of the steps below: their relative order is kept as
+// written.
+__device__ __forceinline__ uint64_t pair(float a, float b)
 {
-    float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        float y0, y1;
-        fma2(y0, y1, fl_of(s[i]), fl_of(s[i + 1]), c, c, bias, bias);
-        const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
-        fma2(sum0, sum1, e0, e1, 1.0f, 1.0f, sum0, sum1);
-        pw[i / 2] = pack_h2(e0, e1);
-    }
-    return sum0 + sum1;
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
 }
-// The same for any mask (bit i: key i seen) and scales: p apart from its factor f, unseen keys 0.
-__device__ __forceinline__ float p32_any(const uint32_t (&s)[32], float c, float bias, float f, uint32_t keep, uint32_t *pw)
+__device__ __forceinline__ void unpair(float &a, float &b, uint64_t d)
 {
-    float sum = 0.0f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2_ord(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2_ord(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm volatile("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float ex2_ord(float x)
+{
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2_ord(float a, float b)
+{
+    uint32_t r;
+    asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// 32 scores -> 16 words of P, and the sums of 2^(s * c + bias).  Written as a software pipeline
+// over groups of four: arguments of group g + 1, ex2 of group g, sums and packing of group g - 1.
+__device__ __forceinline__ void p32(const uint32_t (&s)[32], uint64_t c, uint64_t bias, uint64_t (&sum)[2], uint32_t (&pw)[16])
+{
+    uint64_t y[2][2];
+    float e[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y[0][i] = fma2_ord(pair(fl_of(s[2 * i]), fl_of(s[2 * i + 1])), c, bias);
+#pragma unroll
+    for (int g = 0; g < 9; ++g) {
+        const int cur = g & 1, nxt = cur ^ 1;
+        if (g < 8) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float a, b;
+                unpair(a, b, y[cur][i]);
+                e[cur][2 * i] = ex2_ord(a);
+                e[cur][2 * i + 1] = ex2_ord(b);
+            }
+        }
+        if (g + 1 < 8) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                y[nxt][i] = fma2_ord(pair(fl_of(s[4 * g + 4 + 2 * i]), fl_of(s[4 * g + 5 + 2 * i])), c, bias);
+        }
+        if (g >= 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sum[i] = add2_ord(sum[i], pair(e[nxt][2 * i], e[nxt][2 * i + 1]));
+                pw[2 * g - 2 + i] = pack_h2_ord(e[nxt][2 * i], e[nxt][2 * i + 1]);
+            }
+        }
+    }
+}
+// The same for any mask (unseen keys have the score -inf) and scales, p apart from its factor f:
+// what is not seen is 0 whatever the scales.
+__device__ __forceinline__ void p32_any(const uint32_t (&s)[32], float c, float bias, float f, float (&sum)[4], uint32_t (&pw)[16])
+{
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        const float e0 = (keep >> i) & 1u ? ex2_approx(fmaf(fl_of(s[i]), c, bias)) : 0.0f;
-        const float e1 = (keep >> (i + 1)) & 1u ? ex2_approx(fmaf(fl_of(s[i + 1]), c, bias)) : 0.0f;
-        sum += e0 + e1;
-        pw[i / 2] = pack_h2((keep >> i) & 1u ? e0 * f : 0.0f, (keep >> (i + 1)) & 1u ? e1 * f : 0.0f);
+        const bool k0 = s[i] != kMinusInf, k1 = s[i + 1] != kMinusInf;
+        const float e0 = k0 ? ex2_approx(fmaf(fl_of(s[i]), c, bias)) : 0.0f;
+        const float e1 = k1 ? ex2_approx(fmaf(fl_of(s[i + 1]), c, bias)) : 0.0f;
+        sum[0] += e0;
+        sum[1] += e1;
+        pw[i / 2] = pack_h2(k0 ? e0 * f : 0.0f, k1 ? e1 * f : 0.0f);
     }
-    return sum;
 }
 
 // bits lo..hi-1 (clamped) of a 32-bit mask whose bit 0 is key `at`
@@ -245,9 +328,7 @@ __device__ __forceinline__ uint32_t keep_bits(int at, int lo, int hi)
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    cache_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const CacheAttnArgs A)
+__global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAttnArgs A)
 {
     using S = Sizes<D>;
     constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, false), kIdescPV = idesc_f16_f32(128, D, true);
@@ -256,21 +337,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int64_t range[2];     // flattened start, total
     __shared__ int first[4];         // sequence, head, segment and step of the start
     __shared__ Walk walks[kThreads / 32];
+    __shared__ uint32_t tmem_word;
+    __shared__ int abort_word;
     int *cost = reinterpret_cast<int *>(smem + S::kOffKv);  // steps of a sequence's segments, of one head
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + S::kOffMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
+    volatile int *abort_flag = &abort_word;
     auto bar = [&](int i) -> uint32_t { return sbase + S::kOffBar + 8u * uint32_t(i); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(bar(kBarKvFull + i), 4);
             mbar_init(bar(kBarKvEmpty + i), 1);
-        }
-        for (int i = 0; i < kRaw; ++i) {
-            mbar_init(bar(kBarRawFull + i), 1);
-            mbar_init(bar(kBarRawEmpty + i), 4);
         }
         mbar_init(bar(kBarSEmpty), 4);
         for (int t = 0; t < 2; ++t) {
@@ -284,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == kWarpQK) tmem_alloc(sbase + S::kOffMisc, kTmemCols);
+    if (warp == kWarpQK) tmem_alloc(smem_u32(&tmem_word), kTmemCols);
     // ---- the work: a warp sums a sequence's segments, or with many sequences each thread one's
     if (A.B > 64) {
         for (int b = threadIdx.x; b < A.B; b += kThreads) {
@@ -365,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = tmem_word;
     const int64_t total = range[1], chunk = (total + gridDim.x - 1) / gridDim.x;
     Walk &w = walks[warp];
     if (lane == 0) {
@@ -397,18 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < w.count && ok; ++j, ++g) {
                     const uint32_t st = (2 * g) % kStages;
                     wait(kBarKvFull + st, ((2 * g) / kStages));
-                    const uint32_t kb = sbase + S::kOffKv + st * S::kTileBytes;
+                    const uint64_t kd = sdesc(sbase + S::kOffKv + st * S::kTileBytes, 1024, SWZ_128B);
                     for (int t = 0; t < nt && ok; ++t, ++u) {
                         if (u >= 1) wait(kBarSEmpty, (u - 1));
                         if (!ok) break;
                         tc_fence_after();
                         if (lane != 0) continue;
-                        const uint32_t qa = sbase + S::kOffQ + uint32_t(t) * S::kTileBytes;
+                        // a step of 16 channels is 32 bytes, 64 channels a half tile; in units of 16
+                        const uint64_t qd = sdesc(sbase + S::kOffQ + uint32_t(t) * S::kTileBytes, 1024, SWZ_128B);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t at = uint32_t(kk / 4) * S::kSubBytes + uint32_t(kk % 4) * 32;
-                            mma_f16(tmem + kColS, sdesc(qa + at, 1024, SWZ_128B), sdesc(kb + at, 1024, SWZ_128B),
-                                    kIdescQK, kk > 0);
+                            const uint32_t at = uint32_t(kk / 4) * (S::kSubBytes / 16) + uint32_t(kk % 4) * 2;
+                            mma_f16(tmem + kColS, qd + at, kd + at, kIdescQK, kk > 0);
                         }
                         tc_commit(bar(kBarSFull + t));
                     }
@@ -423,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < w.count && ok; ++j, ++g) {
                     const uint32_t st = (2 * g + 1) % kStages;
                     wait(kBarKvFull + st, ((2 * g + 1) / kStages));
-                    const uint32_t vb = sbase + S::kOffKv + st * S::kTileBytes;
+                    const uint64_t vd = sdesc_mn16(sbase + S::kOffKv + st * S::kTileBytes, S::kSubBytes, 1024);
                     for (int t = 0; t < nt && ok; ++t) {
                         wait(kBarPFull + t, c[t]);
                         if (ok && j == 0 && o[t] >= 1) wait(kBarOEmpty + t, (o[t] - 1));
@@ -433,9 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            mma_f16_ta(tmem + col_o(t), tmem + col_p(t) + 8 * kk,
-                                       sdesc_mn16(vb + 2048 * kk, S::kSubBytes, 1024), kIdescPV,
-                                       (j > 0 || kk > 0) ? 1u : 0u);
+                            mma_f16_ta(tmem + col_o(t), tmem + col_p(t) + 8 * kk, vd + 128 * kk, kIdescPV,
+                                       (j > 0 || kk > 0) ? 1u : 0u);  // 16 rows of 128 bytes a step
                         tc_commit(bar(kBarPvDone + t));
                     }
                     if (ok && lane == 0) tc_commit(bar(kBarKvEmpty + st));
@@ -445,41 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++o[t];
                 }
             }
-        } else if (warp == kWarpLoad) {
-            // ------------------------------------------------------------ codes of K0, K1, V0, V1 of each step
-            uint32_t u = 0;
-            for (; ok && w.open(A); w.next(A)) {
-                int line_l = 0;  // lane i: block i of a window of 32, its first 128-byte line
-                for (int j = 0; j < w.count && ok; ++j) {
-                    if (j % 16 == 0) {
-                        const int blk = w.r.blo + 2 * (w.off + j) + lane;
-                        line_l = 0;
-                        if (blk < w.r.bhi && 2 * j + lane < 2 * w.count) {
-                            const int page = A.table[int64_t(w.b) * A.max_pages + blk];
-                            if (page < 0 || page >= A.num_pages)
-                                record(8);
-                            else
-                                line_l = (page * A.H + w.h) * (D / 2);
-                        }
-                    }
-#pragma unroll 1
-                    for (int k = 0; k < 4 && ok; ++k, ++u) {
-                        const int line = __shfl_sync(0xffffffffu, line_l, 2 * (j % 16) + (k & 1));
-                        const uint32_t st = u % kRaw;
-                        if (u >= kRaw) wait(kBarRawEmpty + st, ((u / kRaw) - 1));
-                        if (ok && lane == 0) {
-                            mbar_arrive_expect_tx(bar(kBarRawFull + st), S::kRawBytes);
-                            tma_load_2d(sbase + S::kOffRaw + st * S::kRawBytes, k < 2 ? &tm_k : &tm_v,
-                                        bar(kBarRawFull + st), 0, line);
-                        }
-                    }
-                }
-            }
-            // tiles in flight land before the block's shared memory is given up
-            if (!ok)
-                for (uint32_t v = u > kRaw ? u - kRaw : 0; v < u; ++v)
-                    for (int i = 0; i < 1 << 20 && !mbar_try_wait(bar(kBarRawFull + v % kRaw), (v / kRaw) & 1); ++i) {
-                    }
         }
     } else if (warp >= kWarpConvert) {
         // ---------------------------------------------------------------- codes to fp16 tiles
@@ -488,68 +530,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kRowsPass = 128 / kRowChunks;  // rows that the 128 threads take at once
         constexpr int kPasses = 64 / kRowsPass;
         const int tid = threadIdx.x - 32 * kWarpConvert, row = tid / kRowChunks, chunk16 = tid % kRowChunks;
-        // TMA's swizzle of 128-byte lines (a line is a row, or two rows at d = 64); a pass is 16 lines
-        const int line = tid / 8;
-        const uint32_t from = uint32_t(line) * 128 + ((uint32_t(tid % 8) ^ uint32_t(line & 7)) << 4);
         // the 16 values are two 16-byte chunks of a row; half of the threads write theirs in the
         // other order, so that a store instruction touches all banks once
         const uint32_t base = uint32_t(chunk16 / 4) * S::kSubBytes + uint32_t(row) * 128;
         const uint32_t c0 = uint32_t(chunk16 % 4) * 2;
         const bool swap = D == 128 ? chunk16 >= 4 : (row & 1) != 0;
-        const uint32_t to0 = base + (((c0 + (swap ? 1 : 0)) ^ uint32_t(row & 7)) << 4);
-        const uint32_t to1 = base + (((c0 + (swap ? 0 : 1)) ^ uint32_t(row & 7)) << 4);
-        uint32_t u = 0, raw = 0;  // fp16 tiles written, tiles of codes read
+        const uint32_t to0 = sbase + S::kOffKv + base + (((c0 + (swap ? 1 : 0)) ^ uint32_t(row & 7)) << 4);
+        const uint32_t to1 = sbase + S::kOffKv + base + (((c0 + (swap ? 0 : 1)) ^ uint32_t(row & 7)) << 4);
+        const uint32_t raw = sbase + S::kOffRaw + uint32_t(tid) * 16;  // this thread's part of a pass
+        uint32_t u = 0, r = 0;  // fp16 tiles written, half tiles of codes read
         for (; ok && w.open(A); w.next(A)) {
-            for (int j = 0; j < 2 * w.count && ok; ++j, ++u) {  // K and V of each step
-                const uint32_t st = u % kStages;
-                if (u >= kStages) wait(kBarKvEmpty + st, ((u / kStages) - 1));
+            // half tile i of the piece: block i & 1 of step i / 4, K (i & 2 = 0) or V
+            const int64_t from = int64_t(w.h) * (kPage * D) + row * D + 16 * chunk16;
+            const int halves = 4 * w.count;
+            int page_l = -1;  // lane k: the page of block k of a window of 32, -1 for none
+            auto fetch = [&](int i, uint32_t slot) {
+                const int j = i / 4;
+                if (i % 64 == 0) {
+                    const int blk = w.r.blo + 2 * (w.off + j) + lane;
+                    page_l = -1;
+                    if (blk < w.r.bhi && 2 * j + lane < halves / 2) {
+                        page_l = A.table[int64_t(w.b) * A.max_pages + blk];
+                        if (page_l < 0 || page_l >= A.num_pages) {
+                            record(8);
+                            page_l = 0;  // its scales are NaN
+                        }
+                    }
+                }
+                const int page = __shfl_sync(0xffffffffu, page_l, 2 * (j % 16) + (i & 1));
+                const int8_t *src = ((i & 2) ? A.v_codes : A.k_codes) + int64_t(max(page, 0)) * A.H * (kPage * D) + from;
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k)
+                    copy_codes(raw + slot * S::kRawBytes + k * 2048, src + k * kRowsPass * D, page >= 0);
+                copy_commit();
+            };
 #pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf, ++raw) {
-                    const uint32_t rs = raw % kRaw;
-                    if (ok) wait(kBarRawFull + rs, (raw / kRaw));
-                    if (!ok) break;
-                    const uint8_t *src = smem + S::kOffRaw + rs * S::kRawBytes + from;
-                    uint8_t *tile = smem + S::kOffKv + st * S::kTileBytes + hf * 64 * 128;
-                    uint4 v[kPasses];
+            for (int i = 0; i < kRaw; ++i) fetch(i, (r + i) % kRaw);  // a piece has a step at least
+#pragma unroll 1
+            for (int i = 0; i < halves; ++i, ++r) {
+                const uint32_t st = u % kStages, slot = r % kRaw;
+                copy_wait<kRaw - 1>();
+                uint4 x[kPasses];
 #pragma unroll
-                    for (int i = 0; i < kPasses; ++i) v[i] = *reinterpret_cast<const uint4 *>(src + i * 16 * 128);
-                    if (w.r.blo + 2 * (w.off + j / 2) + hf >= w.r.bhi) {  // no such block: codes 0
+                for (int k = 0; k < kPasses; ++k) x[k] = ld_shared_u4(raw + slot * S::kRawBytes + k * 2048);
+                if ((i & 1) == 0 && u >= kStages && !wait(kBarKvEmpty + st, (u / kStages) - 1)) break;
+                const uint32_t to = st * S::kTileBytes + uint32_t(i & 1) * (64 * 128);
 #pragma unroll
-                        for (int i = 0; i < kPasses; ++i) v[i] = make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kPasses; ++i) {
-                        const uint32_t wd[4] = {v[i].x ^ 0x80808080u, v[i].y ^ 0x80808080u, v[i].z ^ 0x80808080u,
-                                                v[i].w ^ 0x80808080u};
-                        uint4 a, b;
-                        a.x = bytes_to_h2(wd[0], 0x4140u);
-                        a.y = bytes_to_h2(wd[0], 0x4342u);
-                        a.z = bytes_to_h2(wd[1], 0x4140u);
-                        a.w = bytes_to_h2(wd[1], 0x4342u);
-                        b.x = bytes_to_h2(wd[2], 0x4140u);
-                        b.y = bytes_to_h2(wd[2], 0x4342u);
-                        b.z = bytes_to_h2(wd[3], 0x4140u);
-                        b.w = bytes_to_h2(wd[3], 0x4342u);
-                        *reinterpret_cast<uint4 *>(tile + to0 + i * kRowsPass * 128) = swap ? b : a;
-                        *reinterpret_cast<uint4 *>(tile + to1 + i * kRowsPass * 128) = swap ? a : b;
-                    }
-                    // orders the writes before the tensor core's reads, and the reads of the codes
-                    // before TMA's next writes: without it a read still in flight can be overtaken
+                for (int k = 0; k < kPasses; ++k) {
+                    const uint32_t wd[4] = {x[k].x ^ 0x80808080u, x[k].y ^ 0x80808080u, x[k].z ^ 0x80808080u,
+                                            x[k].w ^ 0x80808080u};
+                    const uint4 a = make_uint4(bytes_to_h2(wd[0], 0x4140u), bytes_to_h2(wd[0], 0x4342u),
+                                               bytes_to_h2(wd[1], 0x4140u), bytes_to_h2(wd[1], 0x4342u));
+                    const uint4 b = make_uint4(bytes_to_h2(wd[2], 0x4140u), bytes_to_h2(wd[2], 0x4342u),
+                                               bytes_to_h2(wd[3], 0x4140u), bytes_to_h2(wd[3], 0x4342u));
+                    st_shared_v4(to0 + to + k * kRowsPass * 128, swap ? b : a);
+                    st_shared_v4(to1 + to + k * kRowsPass * 128, swap ? a : b);
+                }
+                // the part just read is this thread's own, so it may be written again at once
+                if (i + kRaw < halves)
+                    fetch(i + kRaw, slot);
+                else
+                    copy_commit();
+                if (i & 1) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kBarRawEmpty + rs));
+                    if (lane == 0) mbar_arrive(bar(kBarKvFull + st));
+                    ++u;
                 }
-                if (ok && lane == 0) mbar_arrive(bar(kBarKvFull + st));
             }
         }
+        copy_wait<0>();
     } else {
         // ---------------------------------------------------------------- softmax of tile t
         regs_inc<kRegsSoftmax>();
         const int t = warp >> 2, wq = warp & 3;
         const int row = wq * 32 + lane;
         const uint32_t lane_addr = uint32_t(wq * 32) << 16;
-        const uint32_t sa = tmem + lane_addr + kColS, pa = tmem + lane_addr + col_p(t), oa = tmem + lane_addr + col_o(t);
-        uint8_t *qrow = smem + S::kOffQ + uint32_t(t) * S::kTileBytes + row * 128;
+        const uint32_t scales = sbase + S::kOffScale + uint32_t(warp) * 512;
         uint32_t c = 0, o = 0;  // steps and pieces of this tile
         bool split = false;
         const int wk = int(blockIdx.x);
@@ -569,51 +626,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool valid = rr < w.s.n * A.G;
                 const T *src = static_cast<const T *>(A.q) + (int64_t(w.s.ts) + i) * A.q_stride +
                                int64_t(w.h * A.G + rr - i * A.G) * D;
-                float up = 1.0f, down = 1.0f, top = 0.0f;
-                if (valid && A.dtype == 0) {
-#pragma unroll 4
-                    for (int k = 0; k < D; k += 4) {
-                        float f[4];
-                        load4(src + k, f);
-                        top = fmax3(fmaxf(top, fabsf(f[0])), fabsf(f[1]), fmaxf(fabsf(f[2]), fabsf(f[3])));
-                    }
-                    row_power(top, up, down);
+                uint4 x[D / 8];  // all loads in flight at once
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) x[k] = valid ? *reinterpret_cast<const uint4 *>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+                float up = 1.0f, down = 1.0f;
+                if (A.dtype == 0) {
+                    uint32_t top = 0;  // maximum of the bits of |x|, two at a time
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k)
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                                                     __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
+                    row_power(__uint_as_float(max(top & 0xffffu, top >> 16) << 16), up, down);
                 }
                 rc = A.sm_scale * kLog2e * down;
-#pragma unroll 4
-                for (int k = 0; k < D; k += 8) {
-                    float f[8] = {};
-                    if (valid) {
-                        load4(src + k, *reinterpret_cast<float(*)[4]>(&f[0]));
-                        load4(src + k + 4, *reinterpret_cast<float(*)[4]>(&f[4]));
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    uint4 v = x[k];
+                    if (A.dtype == 0) {
+                        uint32_t *w4 = &v.x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w4[e] = pack_h2(__uint_as_float(w4[e] << 16) * up, __uint_as_float(w4[e] & 0xffff0000u) * up);
                     }
-                    uint4 v;
-                    v.x = pack_h2(f[0] * up, f[1] * up);
-                    v.y = pack_h2(f[2] * up, f[3] * up);
-                    v.z = pack_h2(f[4] * up, f[5] * up);
-                    v.w = pack_h2(f[6] * up, f[7] * up);
-                    *reinterpret_cast<uint4 *>(qrow + (k / 64) * S::kSubBytes + ((((k / 8) & 7) ^ (row & 7)) << 4)) = v;
+                    st_shared_v4(sbase + S::kOffQ + uint32_t(t) * S::kTileBytes + (k / 8) * S::kSubBytes + row * 128 +
+                                     (((k & 7) ^ (row & 7)) << 4),
+                                 v);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarQFull + t));
             }
             float m = -INFINITY, l = 0.0f, u = 0.0f;
-            // Scales of 16 steps at a time, lane i those of block i: scale_k; f = 2^5 scale_v / u, its
-            // logarithm and inverse.
-            float sk_l = 0.0f, f_l = 0.0f, g_l = 0.0f, inv_l = 0.0f;
+            // The scales of 16 steps at a time go to shared memory, block by block: scale_k;
+            // f = 2^5 scale_v / u, its logarithm, its inverse.
             for (int j = 0; j < w.count; ++j, ++c) {
                 float su = 1.0f;
                 if (j % 16 == 0) {
+                    __syncwarp();
                     const int blk = w.r.blo + 2 * (w.off + j) + lane;
-                    float sv = 0.0f;
-                    sk_l = 0.0f;
+                    float sv = 0.0f, sk = 0.0f;
                     if (blk < w.r.bhi && 2 * j + lane < 2 * w.count) {
                         const int page = A.table[int64_t(w.b) * A.max_pages + blk];
                         if (page < 0 || page >= A.num_pages) {
-                            sk_l = sv = __int_as_float(0x7fffffff);
+                            sk = sv = __int_as_float(0x7fffffff);
                         } else {
-                            sk_l = A.k_scale[int64_t(page) * A.H + w.h];
+                            sk = A.k_scale[int64_t(page) * A.H + w.h];
                             sv = A.v_scale[int64_t(page) * A.H + w.h];
                         }
                     }
@@ -625,35 +682,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         su = u / u_new;
                         u = u_new;
                     }
-                    f_l = sv == 0.0f ? 0.0f : 32.0f * (sv / u);
-                    const bool plain = f_l > 1e-15f && f_l < INFINITY;
-                    g_l = plain ? log2f(f_l) : 0.0f;
-                    inv_l = plain ? 1.0f / f_l : 0.0f;  // 0: f must be applied apart from the exponent
+                    const float f = sv == 0.0f ? 0.0f : 32.0f * (sv / u);
+                    const bool plain = f > 1e-15f && f < INFINITY;  // else f is applied apart from the exponent
+                    st_shared_v4(scales + 16 * lane, make_uint4(__float_as_uint(sk), __float_as_uint(f),
+                                                                __float_as_uint(plain ? log2f(f) : 0.0f),
+                                                                __float_as_uint(plain ? 1.0f / f : 0.0f)));
+                    __syncwarp();
                 }
-                const int jj = 2 * (j % 16), t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
-                const float c0 = rc * __shfl_sync(0xffffffffu, sk_l, jj), c1 = rc * __shfl_sync(0xffffffffu, sk_l, jj + 1);
-                const float inv0 = __shfl_sync(0xffffffffu, inv_l, jj), inv1 = __shfl_sync(0xffffffffu, inv_l, jj + 1);
-                const bool plain = inv0 > 0.0f && inv1 > 0.0f && lo <= t0 && hi >= t0 + 2 * kPage;
-
-                if (ok) wait(kBarSFull + t, c);
+                float c0, c1;
+                bool fast;
+                {
+                    const float4 b0 = ld_shared_f4(scales + 32 * (j % 16)), b1 = ld_shared_f4(scales + 32 * (j % 16) + 16);
+                    const int t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
+                    c0 = rc * b0.x;
+                    c1 = rc * b1.x;
+                    fast = __all_sync(0xffffffffu, b0.w > 0.0f && b1.w > 0.0f && lo <= t0 && hi >= t0 + 2 * kPage);
+                }
+                if (!wait(kBarSFull + t, c)) break;
                 uint32_t s[4][32];
-                if (ok) {
-                    tc_fence_after();
+                tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld32_nowait(sa + 32 * k, s[k]);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                for (int k = 0; k < 4; ++k) tmem_ld32_nowait(tmem + lane_addr + kColS + 32 * k, s[k]);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) regs_ready(s[k]);
-                }
-                const bool fast = __all_sync(0xffffffffu, plain);
-                uint32_t keep[4];
+                for (int k = 0; k < 4; ++k) regs_ready(s[k]);
                 if (!fast) {
+                    const int t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        keep[k] = keep_bits(t0 + 32 * k, lo, hi);
+                        const uint32_t keep = keep_bits(t0 + 32 * k, lo, hi);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!((keep[k] >> e) & 1u)) s[k][e] = 0xff800000u;  // -inf
+                            if (!((keep >> e) & 1u)) s[k][e] = kMinusInf;
                     }
                 }
                 // the scales are not negative, so they commute with the maximum (0 * -inf is
@@ -663,60 +723,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarSEmpty));
 
-                float alpha = 1.0f;
+                float f = su;  // what acc is rescaled by
                 if (top > m + kGrow || (m == -INFINITY && top > m)) {
-                    alpha = ex2_approx(m - top);
+                    const float alpha = ex2_approx(m - top);
+                    f *= alpha;
+                    l *= alpha;
                     m = top;
                 }
-                const float ref = m == -INFINITY ? 0.0f : m;
-                l *= alpha;
                 // P's columns and acc are free once P . V of the step before is done
-                if (c >= 1 && ok) wait(kBarPvDone + t, (c - 1));
+                if (c >= 1 && !wait(kBarPvDone + t, c - 1)) break;
                 tc_fence_after();
+                const float ref = m == -INFINITY ? 0.0f : m;
+                const float4 b0 = ld_shared_f4(scales + 32 * (j % 16)), b1 = ld_shared_f4(scales + 32 * (j % 16) + 16);
                 if (fast) {
-                    const float g0 = __shfl_sync(0xffffffffu, g_l, jj) - ref, g1 = __shfl_sync(0xffffffffu, g_l, jj + 1) - ref;
-                    uint32_t pw[32];
-                    float s0 = p32(s[0], c0, g0, pw);
-                    s0 += p32(s[1], c0, g0, pw + 16);
-                    if (ok) tmem_st32(pa, pw);
-                    float s1 = p32(s[2], c1, g1, pw);
-                    s1 += p32(s[3], c1, g1, pw + 16);
-                    if (ok) tmem_st32(pa + 32, pw);
-                    l += s0 * inv0 + s1 * inv1;
-                } else {
-                    const float f0 = __shfl_sync(0xffffffffu, f_l, jj), f1 = __shfl_sync(0xffffffffu, f_l, jj + 1);
-                    uint32_t pw[32];
-                    l += p32_any(s[0], c0, -ref, f0, keep[0], pw) + p32_any(s[1], c0, -ref, f0, keep[1], pw + 16);
-                    if (ok) tmem_st32(pa, pw);
-                    l += p32_any(s[2], c1, -ref, f1, keep[2], pw) + p32_any(s[3], c1, -ref, f1, keep[3], pw + 16);
-                    if (ok) tmem_st32(pa + 32, pw);
-                }
-                if (ok) {
-                    const float f = alpha * su;
-                    if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-#pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
-                            uint32_t r[32];
-                            tmem_ld32_wait(oa + 32 * k, r);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float x, y;
-                                mul2(x, y, fl_of(r[e]), fl_of(r[e + 1]), f, f);
-                                r[e] = __float_as_uint(x);
-                                r[e + 1] = __float_as_uint(y);
-                            }
-                            tmem_st32(oa + 32 * k, r);
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t pw[16];
+                        uint64_t sum[2] = {0, 0};
+                        const float cc = k < 2 ? c0 : c1, bias = (k < 2 ? b0.z : b1.z) - ref;
+                        p32(s[k], pair(cc, cc), pair(bias, bias), sum, pw);
+                        tmem_st16(tmem + lane_addr + col_p(t) + 16 * k, pw);
+                        float x0, x1, x2, x3;
+                        unpair(x0, x1, sum[0]);
+                        unpair(x2, x3, sum[1]);
+                        l = fmaf((x0 + x1) + (x2 + x3), k < 2 ? b0.w : b1.w, l);
                     }
-                    tmem_st_wait();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t pw[16];
+                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        p32_any(s[k], k < 2 ? c0 : c1, -ref, k < 2 ? b0.y : b1.y, sum, pw);
+                        tmem_st16(tmem + lane_addr + col_p(t) + 16 * k, pw);
+                        l += sum[0] + sum[1];
+                    }
                 }
+                if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t r[32];
+                        tmem_ld32_wait(tmem + lane_addr + col_o(t) + 32 * k, r);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float x, y;
+                            mul2(x, y, fl_of(r[e]), fl_of(r[e + 1]), f, f);
+                            r[e] = __float_as_uint(x);
+                            r[e + 1] = __float_as_uint(y);
+                        }
+                        tmem_st32(tmem + lane_addr + col_o(t) + 32 * k, r);
+                    }
+                }
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarPFull + t));
             }
             // ---- epilogue of the piece
-            if (ok) wait(kBarOFull + t, o);
-            if (ok) {
+            if (!ok || !wait(kBarOFull + t, o)) break;
+            {
                 tc_fence_after();
                 const int rr = w.p * kRowsSeg + t * 128 + row, i = rr / A.G;
                 const bool valid = rr < w.s.n * A.G;
@@ -738,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int k = 0; k < D / 32; ++k) {
                     uint32_t r[32];
-                    tmem_ld32_wait(oa + 32 * k, r);
+                    tmem_ld32_wait(tmem + lane_addr + col_o(t) + 32 * k, r);
                     if (!valid) continue;
                     if (whole) {
                         T *dst = static_cast<T *>(A.o) + at * D + 32 * k;
@@ -777,12 +841,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, int D>
-cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms, cudaStream_t st)
+cudaError_t launch_for(const CacheAttnArgs &a, int sms, cudaStream_t st)
 {
     cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(Sizes<D>::kAlloc));
     if (e != cudaSuccess) return e;
-    cache_chunk_kernel<T, D><<<sms, kThreads, Sizes<D>::kAlloc, st>>>(tm_k, tm_v, a);
+    cache_chunk_kernel<T, D><<<sms, kThreads, Sizes<D>::kAlloc, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -793,13 +857,12 @@ size_t cache_chunk_part_bytes(int sms, int d)
     return size_t(2) * sms * size_t(d == 128 ? Sizes<128>::kPart : Sizes<64>::kPart) * 4;
 }
 
-cudaError_t launch_cache_chunk(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms,
-                               cudaStream_t st)
+cudaError_t launch_cache_chunk(const CacheAttnArgs &a, int sms, cudaStream_t st)
 {
     if (a.dtype == 0)
-        return a.d == 128 ? launch_for<__nv_bfloat16, 128>(tm_k, tm_v, a, sms, st)
-                          : launch_for<__nv_bfloat16, 64>(tm_k, tm_v, a, sms, st);
-    return a.d == 128 ? launch_for<__half, 128>(tm_k, tm_v, a, sms, st) : launch_for<__half, 64>(tm_k, tm_v, a, sms, st);
+        return a.d == 128 ? launch_for<__nv_bfloat16, 128>(a, sms, st)
+                          : launch_for<__nv_bfloat16, 64>(a, sms, st);
+    return a.d == 128 ? launch_for<__half, 128>(a, sms, st) : launch_for<__half, 64>(a, sms, st);
 }
 
 cudaError_t read_and_clear_cache_chunk_status(int *status)

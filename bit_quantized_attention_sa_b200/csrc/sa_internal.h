@@ -165,8 +165,7 @@ cudaError_t read_and_clear_cache_attn_status(int *status);
 // joins split segments afterwards.
 constexpr int kCacheChunkMaxSeqs = 4096;
 size_t cache_chunk_part_bytes(int sms, int d);
-cudaError_t launch_cache_chunk(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms,
-                               cudaStream_t st);
+cudaError_t launch_cache_chunk(const CacheAttnArgs &a, int sms, cudaStream_t st);
 cudaError_t read_and_clear_cache_chunk_status(int *status);
 // Reads and clears the device status word of the current device (synchronous).
 cudaError_t read_and_clear_status(int *status);
