@@ -44,7 +44,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarpConvert = 8, kWarpQK = 12, kWarpPV = 13;
 constexpr int kStages = 4;  // fp16 tiles
-constexpr int kRaw = 3;     // half tiles (64 tokens) of codes on their way
+constexpr int kRaw = 2;     // tiles of codes on their way
+constexpr int kWindow = 16;  // steps whose scales are in shared memory, in kWindows turns
+constexpr int kWindows = 4;
 constexpr int kRowsSeg = 256;
 constexpr uint32_t kTmemCols = 512, kColS = 0;
 __host__ __device__ constexpr uint32_t col_p(int t) { return 128u + 64u * uint32_t(t); }
@@ -58,22 +60,6 @@ constexpr uint32_t kMinusInf = 0xff800000u;
 constexpr int kBarQFull = 0, kBarKvFull = 2, kBarKvEmpty = kBarKvFull + kStages, kBarSFull = kBarKvEmpty + kStages,
               kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 1, kBarPvDone = kBarPFull + 2,
               kBarOFull = kBarPvDone + 2, kBarOEmpty = kBarOFull + 2, kNumBars = kBarOEmpty + 2;
-
-template <int D>
-struct Sizes {
-    static constexpr int kSub = D / 64;                      // 64-channel halves of a tile
-    static constexpr uint32_t kSubBytes = 128 * 128;         // 128 rows x 128 bytes
-    static constexpr uint32_t kTileBytes = kSub * kSubBytes; // a Q, K or V tile in fp16
-    static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kTileBytes;
-    static constexpr uint32_t kRawBytes = 64 * D;
-    static constexpr uint32_t kOffRaw = kOffKv + kStages * kTileBytes;
-    static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
-    static constexpr uint32_t kOffScale = (kOffBar + 8 * kNumBars + 15) & ~15u;  // of 8 warps, 32 blocks
-    static constexpr uint32_t kAlloc = kOffScale + 8 * 32 * 16 + 1024;
-    static constexpr int kPart = kRowsSeg * (D + 2);
-};
-static_assert(Sizes<128>::kAlloc <= 227 * 1024 - 1200, "shared memory per CTA");
-static_assert(4 * kCacheChunkMaxSeqs <= kStages * Sizes<64>::kTileBytes, "the costs fit the ring before it is used");
 
 template <uint32_t NR>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NR)); }
@@ -160,6 +146,24 @@ private:
     }
 };
 
+template <int D>
+struct Sizes {
+    static constexpr int kSub = D / 64;                      // 64-channel halves of a tile
+    static constexpr uint32_t kSubBytes = 128 * 128;         // 128 rows x 128 bytes
+    static constexpr uint32_t kTileBytes = kSub * kSubBytes; // a Q, K or V tile in fp16
+    static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kTileBytes;
+    static constexpr uint32_t kRawBytes = 128 * D;
+    static constexpr uint32_t kOffRaw = kOffKv + kStages * kTileBytes;
+    static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawBytes;
+    static constexpr uint32_t kOffBar = kOffScale + kWindows * 2 * kWindow * 8;
+    static constexpr uint32_t kOffWalk = kOffBar + 8 * (kNumBars + 1);
+    static constexpr uint32_t kOffMisc = kOffWalk + uint32_t(sizeof(Walk)) * (kWarpPV + 1);
+    static constexpr uint32_t kAlloc = kOffMisc + 48;  // range, first, tensor memory's address, abort flag
+    static constexpr int kPart = kRowsSeg * (D + 2);
+};
+static_assert(Sizes<128>::kAlloc <= 227 * 1024, "shared memory per CTA");
+static_assert(4 * kCacheChunkMaxSeqs <= kStages * Sizes<64>::kTileBytes, "the costs fit the ring before it is used");
+
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32])
 {
     asm volatile(
@@ -203,6 +207,10 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr)
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ void st_shared_f2(uint32_t addr, float a, float b)
+{
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
 {
@@ -332,17 +340,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
 {
     using S = Sizes<D>;
     constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, false), kIdescPV = idesc_f16_f32(128, D, true);
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ int64_t range[2];     // flattened start, total
-    __shared__ int first[4];         // sequence, head, segment and step of the start
-    __shared__ Walk walks[kThreads / 32];
-    __shared__ uint32_t tmem_word;
-    __shared__ int abort_word;
+    // All shared memory is dynamic, so that it starts at the 1024-byte boundary that the tiles need.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    int64_t *range = reinterpret_cast<int64_t *>(smem + S::kOffMisc);   // flattened start, total
+    int *first = reinterpret_cast<int *>(smem + S::kOffMisc + 16);      // sequence, head, segment and step of the start
+    uint32_t *tmem_word = reinterpret_cast<uint32_t *>(smem + S::kOffMisc + 32);
     int *cost = reinterpret_cast<int *>(smem + S::kOffKv);  // steps of a sequence's segments, of one head
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int *abort_flag = &abort_word;
+    volatile int *abort_flag = reinterpret_cast<int *>(smem + S::kOffMisc + 36);
+    if (sbase & 1023u) {  // never so far; the tiles would be read wrongly
+        if (threadIdx.x == 0) record(6);
+        return;
+    }
     auto bar = [&](int i) -> uint32_t { return sbase + S::kOffBar + 8u * uint32_t(i); };
 
     if (threadIdx.x == 0) {
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == kWarpQK) tmem_alloc(smem_u32(&tmem_word), kTmemCols);
+    if (warp == kWarpQK) tmem_alloc(smem_u32(tmem_word), kTmemCols);
     // ---- the work: a warp sums a sequence's segments, or with many sequences each thread one's
     if (A.B > 64) {
         for (int b = threadIdx.x; b < A.B; b += kThreads) {
@@ -443,10 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         }
     }
     __syncthreads();
-    const uint32_t tmem = tmem_word;
+    const uint32_t tmem = *tmem_word;
     const int64_t total = range[1], chunk = (total + gridDim.x - 1) / gridDim.x;
-    Walk &w = walks[warp];
-    if (lane == 0) {
+    Walk &w = reinterpret_cast<Walk *>(smem + S::kOffWalk)[min(warp, kWarpPV)];
+    if (lane == 0 && warp <= kWarpPV) {
         w.pos = range[0];
         w.end = min(total, chunk * (int64_t(blockIdx.x) + 1));
         w.pieces = 0;
@@ -480,17 +490,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                         if (u >= 1) wait(kBarSEmpty, (u - 1));
                         if (!ok) break;
                         tc_fence_after();
-                        if (lane != 0) continue;
                         // a step of 16 channels is 32 bytes, 64 channels a half tile; in units of 16
                         const uint64_t qd = sdesc(sbase + S::kOffQ + uint32_t(t) * S::kTileBytes, 1024, SWZ_128B);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t at = uint32_t(kk / 4) * (S::kSubBytes / 16) + uint32_t(kk % 4) * 2;
-                            mma_f16(tmem + kColS, qd + at, kd + at, kIdescQK, kk > 0);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t at = uint32_t(kk / 4) * (S::kSubBytes / 16) + uint32_t(kk % 4) * 2;
+                                mma_f16(tmem + kColS, qd + at, kd + at, kIdescQK, kk > 0);
+                            }
+                            tc_commit(bar(kBarSFull + t));
+                            if (t == nt - 1) tc_commit(bar(kBarKvEmpty + st));
                         }
-                        tc_commit(bar(kBarSFull + t));
+                        __syncwarp();
                     }
-                    if (ok && lane == 0) tc_commit(bar(kBarKvEmpty + st));
                 }
             }
         } else if (warp == kWarpPV) {
@@ -507,96 +519,102 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                         if (ok && j == 0 && o[t] >= 1) wait(kBarOEmpty + t, (o[t] - 1));
                         if (!ok) break;
                         ++c[t];
-                        if (lane != 0) continue;
                         tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_f16_ta(tmem + col_o(t), tmem + col_p(t) + 8 * kk, vd + 128 * kk, kIdescPV,
-                                       (j > 0 || kk > 0) ? 1u : 0u);  // 16 rows of 128 bytes a step
-                        tc_commit(bar(kBarPvDone + t));
+                            for (int kk = 0; kk < 8; ++kk)  // 16 rows of 128 bytes a step
+                                mma_f16_ta(tmem + col_o(t), tmem + col_p(t) + 8 * kk, vd + 128 * kk, kIdescPV,
+                                           (j > 0 || kk > 0) ? 1u : 0u);
+                            tc_commit(bar(kBarPvDone + t));
+                            if (j == w.count - 1) tc_commit(bar(kBarOFull + t));
+                            if (t == nt - 1) tc_commit(bar(kBarKvEmpty + st));
+                        }
+                        __syncwarp();
                     }
-                    if (ok && lane == 0) tc_commit(bar(kBarKvEmpty + st));
                 }
-                for (int t = 0; t < nt && ok; ++t) {
-                    if (lane == 0) tc_commit(bar(kBarOFull + t));
-                    ++o[t];
-                }
+                for (int t = 0; t < nt; ++t) ++o[t];
             }
         }
     } else if (warp >= kWarpConvert) {
         // ---------------------------------------------------------------- codes to fp16 tiles
         regs_dec<kRegsConvert>();
-        constexpr int kRowChunks = D / 16;           // 16-byte chunks of a row of codes
-        constexpr int kRowsPass = 128 / kRowChunks;  // rows that the 128 threads take at once
-        constexpr int kPasses = 64 / kRowsPass;
-        const int tid = threadIdx.x - 32 * kWarpConvert, row = tid / kRowChunks, chunk16 = tid % kRowChunks;
-        // the 16 values are two 16-byte chunks of a row; half of the threads write theirs in the
-        // other order, so that a store instruction touches all banks once
-        const uint32_t base = uint32_t(chunk16 / 4) * S::kSubBytes + uint32_t(row) * 128;
-        const uint32_t c0 = uint32_t(chunk16 % 4) * 2;
-        const bool swap = D == 128 ? chunk16 >= 4 : (row & 1) != 0;
-        const uint32_t to0 = sbase + S::kOffKv + base + (((c0 + (swap ? 1 : 0)) ^ uint32_t(row & 7)) << 4);
-        const uint32_t to1 = sbase + S::kOffKv + base + (((c0 + (swap ? 0 : 1)) ^ uint32_t(row & 7)) << 4);
+        // A thread takes 16-byte chunks of codes at one channel offset, kPasses of them a tile.  The 16
+        // values become two neighbouring 16-byte chunks of a row; eight lanes write two rows of four, so
+        // the swizzle spreads a store over all banks.
+        constexpr int kRowsPass = 2048 / D;  // rows that the 128 threads take at once
+        constexpr int kPasses = 128 / kRowsPass, kHalf = kPasses / 2;
+        const int tid = threadIdx.x - 32 * kWarpConvert, wc = tid / 32;
+        const int chunk16 = lane % 4 + (D == 128 ? 4 * (wc & 1) : 0);
+        const int row = lane / 4 + 8 * (D == 128 ? wc >> 1 : wc);
+        const uint32_t to = sbase + S::kOffKv + uint32_t(chunk16 / 4) * S::kSubBytes + uint32_t(row) * 128;
+        const uint32_t to0 = to + ((uint32_t(chunk16 % 4 * 2) ^ uint32_t(row & 7)) << 4);
+        const uint32_t to1 = to + ((uint32_t(chunk16 % 4 * 2 + 1) ^ uint32_t(row & 7)) << 4);
         const uint32_t raw = sbase + S::kOffRaw + uint32_t(tid) * 16;  // this thread's part of a pass
-        uint32_t u = 0, r = 0;  // fp16 tiles written, half tiles of codes read
+        uint32_t u = 0;  // tiles
         for (; ok && w.open(A); w.next(A)) {
-            // half tile i of the piece: block i & 1 of step i / 4, K (i & 2 = 0) or V
-            const int64_t from = int64_t(w.h) * (kPage * D) + row * D + 16 * chunk16;
-            const int halves = 4 * w.count;
-            int page_l = -1;  // lane k: the page of block k of a window of 32, -1 for none
-            auto fetch = [&](int i, uint32_t slot) {
-                const int j = i / 4;
-                if (i % 64 == 0) {
-                    const int blk = w.r.blo + 2 * (w.off + j) + lane;
-                    page_l = -1;
-                    if (blk < w.r.bhi && 2 * j + lane < halves / 2) {
-                        page_l = A.table[int64_t(w.b) * A.max_pages + blk];
-                        if (page_l < 0 || page_l >= A.num_pages) {
-                            record(8);
-                            page_l = 0;  // its scales are NaN
-                        }
+            // tile i of the piece: K of step i / 2 (i even), or V
+            const int tiles = 2 * w.count;
+            // lane k: the page of block k of a window of 16 steps, -1 for none; and of the window after
+            auto window = [&](int j) {
+                const int blk = w.r.blo + 2 * (w.off + j) + lane;
+                int page = -1;
+                if (blk < w.r.bhi && 2 * j + lane < tiles) {
+                    page = A.table[int64_t(w.b) * A.max_pages + blk];
+                    if (page < 0 || page >= A.num_pages) {
+                        record(8);
+                        page = 0;  // its scales are NaN
                     }
                 }
-                const int page = __shfl_sync(0xffffffffu, page_l, 2 * (j % 16) + (i & 1));
-                const int8_t *src = ((i & 2) ? A.v_codes : A.k_codes) + int64_t(max(page, 0)) * A.H * (kPage * D) + from;
+                return page;
+            };
+            const int64_t from = int64_t(w.h) * (kPage * D) + row * D + 16 * chunk16, page_size = int64_t(A.H) * (kPage * D);
+            int page_l = window(0), page_n = window(16);
+            auto fetch = [&](int i, uint32_t slot) {
+                if (i % 32 == 0 && i > 0) {
+                    page_l = page_n;
+                    page_n = window(i / 2 + 16);
+                }
+                const int8_t *codes = ((i & 1) ? A.v_codes : A.k_codes) + from;
 #pragma unroll
-                for (int k = 0; k < kPasses; ++k)
-                    copy_codes(raw + slot * S::kRawBytes + k * 2048, src + k * kRowsPass * D, page >= 0);
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int page = __shfl_sync(0xffffffffu, page_l, 2 * (i / 2 % 16) + hf);
+                    const int8_t *src = codes + max(page, 0) * page_size;
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k)
+                        copy_codes(raw + slot * S::kRawBytes + (hf * kHalf + k) * 2048, src + k * kRowsPass * D, page >= 0);
+                }
                 copy_commit();
             };
 #pragma unroll 1
-            for (int i = 0; i < kRaw; ++i) fetch(i, (r + i) % kRaw);  // a piece has a step at least
+            for (int i = 0; i < kRaw; ++i) fetch(i, (u + i) % kRaw);  // a piece has a step at least
 #pragma unroll 1
-            for (int i = 0; i < halves; ++i, ++r) {
-                const uint32_t st = u % kStages, slot = r % kRaw;
+            for (int i = 0; i < tiles; ++i, ++u) {
+                const uint32_t st = u % kStages, slot = u % kRaw;
                 copy_wait<kRaw - 1>();
                 uint4 x[kPasses];
 #pragma unroll
                 for (int k = 0; k < kPasses; ++k) x[k] = ld_shared_u4(raw + slot * S::kRawBytes + k * 2048);
-                if ((i & 1) == 0 && u >= kStages && !wait(kBarKvEmpty + st, (u / kStages) - 1)) break;
-                const uint32_t to = st * S::kTileBytes + uint32_t(i & 1) * (64 * 128);
+                if (u >= kStages && !wait(kBarKvEmpty + st, u / kStages - 1)) break;
+                const uint32_t at = st * S::kTileBytes;
 #pragma unroll
                 for (int k = 0; k < kPasses; ++k) {
                     const uint32_t wd[4] = {x[k].x ^ 0x80808080u, x[k].y ^ 0x80808080u, x[k].z ^ 0x80808080u,
                                             x[k].w ^ 0x80808080u};
-                    const uint4 a = make_uint4(bytes_to_h2(wd[0], 0x4140u), bytes_to_h2(wd[0], 0x4342u),
-                                               bytes_to_h2(wd[1], 0x4140u), bytes_to_h2(wd[1], 0x4342u));
-                    const uint4 b = make_uint4(bytes_to_h2(wd[2], 0x4140u), bytes_to_h2(wd[2], 0x4342u),
-                                               bytes_to_h2(wd[3], 0x4140u), bytes_to_h2(wd[3], 0x4342u));
-                    st_shared_v4(to0 + to + k * kRowsPass * 128, swap ? b : a);
-                    st_shared_v4(to1 + to + k * kRowsPass * 128, swap ? a : b);
+                    st_shared_v4(to0 + at + k * kRowsPass * 128,
+                                 make_uint4(bytes_to_h2(wd[0], 0x4140u), bytes_to_h2(wd[0], 0x4342u),
+                                            bytes_to_h2(wd[1], 0x4140u), bytes_to_h2(wd[1], 0x4342u)));
+                    st_shared_v4(to1 + at + k * kRowsPass * 128,
+                                 make_uint4(bytes_to_h2(wd[2], 0x4140u), bytes_to_h2(wd[2], 0x4342u),
+                                            bytes_to_h2(wd[3], 0x4140u), bytes_to_h2(wd[3], 0x4342u)));
                 }
-                // the part just read is this thread's own, so it may be written again at once
-                if (i + kRaw < halves)
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarKvFull + st));
+                // the parts just read are this thread's own, so they may be written again
+                if (i + kRaw < tiles)
                     fetch(i + kRaw, slot);
                 else
                     copy_commit();
-                if (i & 1) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kBarKvFull + st));
-                    ++u;
-                }
             }
         }
         copy_wait<0>();
@@ -606,12 +624,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         const int t = warp >> 2, wq = warp & 3;
         const int row = wq * 32 + lane;
         const uint32_t lane_addr = uint32_t(wq * 32) << 16;
-        const uint32_t scales = sbase + S::kOffScale + uint32_t(warp) * 512;
+        uint32_t turn = 0;  // windows of scales so far
         uint32_t c = 0, o = 0;  // steps and pieces of this tile
         bool split = false;
         const int wk = int(blockIdx.x);
         for (; w.open(A); w.next(A)) {
-            if (t >= w.tiles(A)) continue;
+            if (t >= w.tiles(A)) {
+                turn += (w.count + kWindow - 1) / kWindow;
+                continue;
+            }
             int lo, hi;  // the keys that this row sees, [lo, hi); rows past the last see all, and are not written
             {
                 const int rr = w.p * kRowsSeg + t * 128 + row, pos = w.s.len - w.s.n + rr / A.G;
@@ -657,12 +678,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 if (lane == 0) mbar_arrive(bar(kBarQFull + t));
             }
             float m = -INFINITY, l = 0.0f, u = 0.0f;
-            // The scales of 16 steps at a time go to shared memory, block by block: scale_k;
-            // f = 2^5 scale_v / u, its logarithm, its inverse.
+            // The scales of 16 steps at a time go to shared memory, for each block scale_k and
+            // f = 2^5 scale_v / u.  The warps of both tiles write the same values, four windows in turn:
+            // no two warps are that far apart, for each S needs the one before it to have been read.
+            uint32_t scales = 0;
             for (int j = 0; j < w.count; ++j, ++c) {
                 float su = 1.0f;
-                if (j % 16 == 0) {
-                    __syncwarp();
+                if (j % kWindow == 0) {
+                    scales = sbase + S::kOffScale + (turn++ % kWindows) * (2 * kWindow * 8);
                     const int blk = w.r.blo + 2 * (w.off + j) + lane;
                     float sv = 0.0f, sk = 0.0f;
                     if (blk < w.r.bhi && 2 * j + lane < 2 * w.count) {
@@ -682,21 +705,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                         su = u / u_new;
                         u = u_new;
                     }
-                    const float f = sv == 0.0f ? 0.0f : 32.0f * (sv / u);
-                    const bool plain = f > 1e-15f && f < INFINITY;  // else f is applied apart from the exponent
-                    st_shared_v4(scales + 16 * lane, make_uint4(__float_as_uint(sk), __float_as_uint(f),
-                                                                __float_as_uint(plain ? log2f(f) : 0.0f),
-                                                                __float_as_uint(plain ? 1.0f / f : 0.0f)));
+                    st_shared_f2(scales + 8 * lane, sk, sv == 0.0f ? 0.0f : 32.0f * (sv / u));
                     __syncwarp();
                 }
                 float c0, c1;
                 bool fast;
                 {
-                    const float4 b0 = ld_shared_f4(scales + 32 * (j % 16)), b1 = ld_shared_f4(scales + 32 * (j % 16) + 16);
+                    const float4 b = ld_shared_f4(scales + 16 * (j % kWindow));  // of both blocks
                     const int t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
-                    c0 = rc * b0.x;
-                    c1 = rc * b1.x;
-                    fast = __all_sync(0xffffffffu, b0.w > 0.0f && b1.w > 0.0f && lo <= t0 && hi >= t0 + 2 * kPage);
+                    c0 = rc * b.x;
+                    c1 = rc * b.z;
+                    // else f is applied apart from the exponent
+                    fast = __all_sync(0xffffffffu, b.y > 1e-15f && b.y < INFINITY && b.w > 1e-15f && b.w < INFINITY &&
+                                                       lo <= t0 && hi >= t0 + 2 * kPage);
                 }
                 if (!wait(kBarSFull + t, c)) break;
                 uint32_t s[4][32];
@@ -734,26 +755,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 if (c >= 1 && !wait(kBarPvDone + t, c - 1)) break;
                 tc_fence_after();
                 const float ref = m == -INFINITY ? 0.0f : m;
-                const float4 b0 = ld_shared_f4(scales + 32 * (j % 16)), b1 = ld_shared_f4(scales + 32 * (j % 16) + 16);
+                const float4 b = ld_shared_f4(scales + 16 * (j % kWindow));
                 if (fast) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t pw[16];
                         uint64_t sum[2] = {0, 0};
-                        const float cc = k < 2 ? c0 : c1, bias = (k < 2 ? b0.z : b1.z) - ref;
+                        const float cc = k < 2 ? c0 : c1, f = k < 2 ? b.y : b.w, bias = __log2f(f) - ref;
                         p32(s[k], pair(cc, cc), pair(bias, bias), sum, pw);
                         tmem_st16(tmem + lane_addr + col_p(t) + 16 * k, pw);
                         float x0, x1, x2, x3;
                         unpair(x0, x1, sum[0]);
                         unpair(x2, x3, sum[1]);
-                        l = fmaf((x0 + x1) + (x2 + x3), k < 2 ? b0.w : b1.w, l);
+                        l = fmaf((x0 + x1) + (x2 + x3), __frcp_rn(f), l);
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t pw[16];
                         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        p32_any(s[k], k < 2 ? c0 : c1, -ref, k < 2 ? b0.y : b1.y, sum, pw);
+                        p32_any(s[k], k < 2 ? c0 : c1, -ref, k < 2 ? b.y : b.w, sum, pw);
                         tmem_st16(tmem + lane_addr + col_p(t) + 16 * k, pw);
                         l += sum[0] + sum[1];
                     }

@@ -431,6 +431,14 @@ __device__ __forceinline__ void tmem_st_wait()
 
 // ------------------------------------------------------------------ misc
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // Orders this thread's generic-proxy shared-memory writes before later async-proxy
 // reads (the tensor core reading P).
 __device__ __forceinline__ void fence_proxy_async_smem()
