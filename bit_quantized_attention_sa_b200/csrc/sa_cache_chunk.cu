@@ -51,7 +51,7 @@ constexpr int kRowsSeg = 256;
 constexpr uint32_t kTmemCols = 512, kColS = 0;
 __host__ __device__ constexpr uint32_t col_p(int t) { return 128u + 64u * uint32_t(t); }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * uint32_t(t); }
-constexpr uint32_t kRegsSoftmax = 176, kRegsConvert = 112, kRegsIssue = 48, kLaunchRegs = 128;
+constexpr uint32_t kRegsSoftmax = 176, kRegsConvert = 88, kRegsIssue = 72, kLaunchRegs = 128;
 static_assert(128 * (2 * kRegsSoftmax + kRegsConvert + kRegsIssue) <= kLaunchRegs * kThreads,
               "the register split must fit the registers the block is launched with");
 constexpr float kGrow = 8.0f;
