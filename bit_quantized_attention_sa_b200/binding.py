@@ -6,7 +6,6 @@ fallback: importing this module raises if the library has not been built.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -23,6 +22,13 @@ if not os.path.exists(_LIB_PATH):
         " (there is no CPU fallback)")
 
 _lib = ctypes.CDLL(_LIB_PATH)
+
+try:
+    from . import _sa_torch  # the serving calls' torch side, which calls the same library
+except ImportError as e:
+    raise ImportError(f"_sa_torch.so in {_PKG} is missing or does not fit this PyTorch: build it with"
+                      " `python -m bit_quantized_attention_sa_b200.build`") from e
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -420,9 +426,12 @@ def sa_sla_fwd(q, k, v, classes, sm_scale: float | None = None, phi: int = SA_PH
 
 # ---- generation over a cache: rotary positions, the paged INT8 cache, attention over it
 
+# These calls recur for every layer of a decoding step, so their checks and marshalling are
+# compiled (csrc/sa_torch.cpp); wrong tensors raise ValueError there, a library status SAError.
+_sa_torch.set_error(SAError)
+
 CACHE_PAGE = 64  # tokens of a page
 _ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class SACache(NamedTuple):
@@ -442,24 +451,6 @@ def sa_cache_alloc(pages: int, heads: int, d: int = 128, device="cuda") -> SACac
     return SACache(*half(), *half())
 
 
-class _RopeTensor(ctypes.Structure):
-    _fields_ = [("x", _P), ("y", _P), ("x_batch", _L), ("x_head", _L), ("x_tok", _L), ("y_batch", _L), ("y_head", _L),
-                ("y_tok", _L), ("heads", _I)]
-
-
-def _on(device: torch.device):
-    """The device of the tensors as the current one for a launch (the library launches on the
-    current device)."""
-    return _SAME if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-_SAME = contextlib.nullcontext()
-
-
-def _raw_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def sa_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
                         original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
     """(freqs fp64 [rot / 2], amplitude) for sa_rope; scaling "plain", "linear", "base" or
@@ -474,14 +465,6 @@ def sa_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain",
     return freqs.to(device), amplitude.value
 
 
-def _rope_view(t: torch.Tensor):
-    """(B, N, batch, head and token strides, heads) of [B, H, N, d], or of packed [T, H, d]."""
-    step = [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]  # of a single one: any number
-    if t.dim() == 4:
-        return t.shape[0], t.shape[2], step[0], step[1], step[2], t.shape[1]
-    return 1, t.shape[0], 0, step[1], step[0], t.shape[1]
-
-
 def sa_rope(q, k, pos, freqs, rot: int | None = None, interleaved: bool = False, sections=None, amplitude: float = 1.0,
             inverse: bool = False, out=None):
     """Rotary positions of q and k (k may be None), [B, H, N, d] or packed tokens [T, H, d] of
@@ -491,105 +474,26 @@ def sa_rope(q, k, pos, freqs, rot: int | None = None, interleaved: bool = False,
     sa_rope_frequencies; rot defaults to d.  inverse turns back (times amplitude): the
     transposed map.  out: (q', k') or q' to write, which may be the inputs themselves.
     Returns (q', k'), or q' without k."""
-    xs = (q,) if k is None else (q, k)
-    dtype, device, dim = q.dtype, q.device, q.dim()
-    for t in xs:
-        if not t.is_cuda or t.dtype not in _DTYPES or t.dim() not in (3, 4) or t.stride(-1) != 1:
-            raise ValueError("q and k must be bf16, fp16 or fp32 CUDA tensors [B, H, N, d] or [T, H, d] with contiguous channels")
-        if t.dtype != dtype or t.device != device or t.dim() != dim or t.shape[-1] != q.shape[-1]:
-            raise ValueError("q and k differ in dtype, device, layout or head size")
-    B, N = _rope_view(q)[:2]
-    if k is not None and _rope_view(k)[:2] != (B, N):
-        raise ValueError("q and k have different tokens")
-    ys = (out,) if isinstance(out, torch.Tensor) else out
-    if ys is None:
-        ys = tuple(torch.empty(t.shape, dtype=dtype, device=device) for t in xs)
-    if len(ys) != len(xs):
-        raise ValueError("out must match q and k")
-    for x, y in zip(xs, ys):
-        if y.dtype != dtype or y.device != device or y.shape != x.shape or y.stride(-1) != 1:
-            raise ValueError("out must have q's and k's dtypes, devices and shapes, with contiguous channels")
-    d = q.shape[-1]
-    rot = d if rot is None else int(rot)
-    axes = 1 if sections is None else len(sections)
-    lead = 0 if sections is None else 1
-    if pos.dtype != torch.int32 or pos.device != device or not pos.is_contiguous():
-        raise ValueError("pos must be a contiguous int32 tensor on q's device")
-    shape = tuple(pos.shape)
-    if (lead and (not shape or shape[0] != axes)) or shape[lead:] not in ((N,), (B, N)):
-        raise ValueError("pos must be [N], [B, N] or [T], after one row for each section")
-    per_batch = len(shape) - lead == 2
-    if freqs.dtype != torch.float64 or freqs.device != device or not freqs.is_contiguous() or freqs.numel() != rot // 2:
-        raise ValueError("freqs must be a contiguous fp64 tensor of rot / 2 values on q's device")
-    arr = (_RopeTensor * len(xs))()
-    for a, x, y in zip(arr, xs, ys):
-        _, _, a.x_batch, a.x_head, a.x_tok, a.heads = _rope_view(x)
-        _, _, a.y_batch, a.y_head, a.y_tok, _ = _rope_view(y)
-        a.x, a.y = x.data_ptr(), y.data_ptr()
-    secs = None if sections is None else (_I * axes)(*[int(n) for n in sections])
-    with _on(device):
-        _check(_lib.sa_rope(arr, len(xs), _DTYPES[dtype], B, N, d, rot, bool(interleaved), pos.data_ptr(),
-                            N * (B if per_batch else 1), N if per_batch else 0, axes, secs, freqs.data_ptr(),
-                            float(amplitude), bool(inverse), _raw_stream(device)), "sa_rope")
-    return ys[0] if k is None else tuple(ys)
-
-
-def _cache_call(cache, tok_start, kv_lens, page_table, device):
-    """Checks the cache and the sequences' arrays; returns the tail of a call's arguments."""
-    kc, ks, vc, vs = cache
-    pages, H, rows, d = kc.shape if kc.dim() == 4 else (0, 0, 0, 0)
-    if kc.dtype != torch.int8 or rows != CACHE_PAGE or kc.shape != vc.shape or vc.dtype != torch.int8:
-        raise ValueError("the cache's codes must be int8 [pages, heads, 64, d]")
-    if ks.dtype != torch.float32 or vs.dtype != torch.float32 or ks.shape != (pages, H) or vs.shape != (pages, H):
-        raise ValueError("the cache's scales must be fp32 [pages, heads]")
-    B = kv_lens.numel()
-    if tok_start.dtype != torch.int32 or kv_lens.dtype != torch.int32 or page_table.dtype != torch.int32 \
-            or kv_lens.dim() != 1 or tok_start.shape != (B + 1,) or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("tok_start, kv_lens and page_table must be int32 [B + 1], [B] and [B, max_pages]")
-    for t in (kc, ks, vc, vs, tok_start, kv_lens, page_table):
-        if t.device != device or not t.is_contiguous():
-            raise ValueError("the cache and the sequences' arrays must be contiguous, on the tokens' device")
-    return (tok_start.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), B, page_table.shape[1], kc.data_ptr(),
-            ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, H), d
-
-
-def _token_arg(t: torch.Tensor, H: int, d: int, name: str) -> int:
-    """Checks packed tokens [T, H, d] (strided over tokens only); returns the token stride."""
-    if not t.is_cuda or t.dtype not in (torch.bfloat16, torch.float16) or t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
-        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [T, {H}, {d}]")
-    if t.shape[0] == 0:
-        return H * d
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}'s heads must follow each other without a gap")
-    return t.stride(0) if t.shape[0] > 1 else H * d
+    out_q = out_k = None
+    if out is not None:
+        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != (1 if k is None else 2):
+            raise ValueError("out must match q and k")
+        out_q, out_k = outs[0], outs[-1] if k is not None else None
+    return _sa_torch.rope(q, k, pos, freqs, rot, interleaved, sections, amplitude, inverse, out_q, out_k)
 
 
 def sa_cache_append(cache, k, v, tok_start, kv_lens, page_table) -> None:
     """Writes the new tokens k, v [T, heads, d] (bf16 or fp16; token strides as from a slice of
     a fused projection) into the cache.  kv_lens int32 [B] counts each sequence's tokens
     including the new ones, which are rows tok_start[b] .. tok_start[b + 1] - 1."""
-    args, d = _cache_call(cache, tok_start, kv_lens, page_table, k.device)
-    H = args[-1]
-    ks, vs = _token_arg(k, H, d, "k"), _token_arg(v, H, d, "v")
-    if v.dtype != k.dtype or v.device != k.device or v.shape != k.shape:
-        raise ValueError("k and v differ in dtype, device or shape")
-    with _on(k.device):
-        _check(_lib.sa_cache_append(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.shape[0], ks, vs, *args, d,
-                                    _raw_stream(k.device)), "sa_cache_append")
+    _sa_torch.append(*cache, k, v, tok_start, kv_lens, page_table)
 
 
 def sa_cache_read(cache, tokens: int, tok_start, kv_lens, page_table, dtype=torch.bfloat16):
     """The values (k, v), each [tokens, heads, d] of dtype (bf16, fp16 or fp32), of the tokens
     at tok_start / kv_lens: the last tok_start[b + 1] - tok_start[b] of each sequence."""
-    device = cache[0].device
-    if not cache[0].is_cuda or dtype not in _DTYPES:
-        raise ValueError("the cache must be on a CUDA device and dtype bf16, fp16 or fp32")
-    args, d = _cache_call(cache, tok_start, kv_lens, page_table, device)
-    k, v = (torch.empty((int(tokens), args[-1], d), dtype=dtype, device=device) for _ in range(2))
-    with _on(device):
-        _check(_lib.sa_cache_read(k.data_ptr(), v.data_ptr(), _DTYPES[dtype], k.shape[0], *args, d,
-                                  _raw_stream(device)), "sa_cache_read")
-    return k, v
+    return _sa_torch.read(*cache, tokens, tok_start, kv_lens, page_table, dtype)
 
 
 def sa_cache_attn(cache, q, tok_start, kv_lens, page_table, causal: bool = True, window: int = 0,
@@ -600,26 +504,7 @@ def sa_cache_attn(cache, q, tok_start, kv_lens, page_table, causal: bool = True,
     window > 0).  The query heads are a multiple of the cache's heads; heads that follow each
     other share one.  Returns o [T, query heads, d], and lse fp32 [T, query heads] with
     return_lse; 0 and -inf for a query that sees nothing."""
-    args, d = _cache_call(cache, tok_start, kv_lens, page_table, q.device)
-    H = args[-1]
-    Hq = q.shape[1] if q.dim() == 3 else 0
-    if Hq < 1 or Hq % H != 0:
-        raise ValueError("q must be [T, query heads, d] with a multiple of the cache's heads")
-    stride, T, device = _token_arg(q, Hq, d, "q"), q.shape[0], q.device
-    o = torch.empty((T, Hq, d), dtype=q.dtype, device=device) if out is None else out
-    if o.dtype != q.dtype or o.device != device or o.shape != q.shape or not o.is_contiguous():
-        raise ValueError("out must be a contiguous tensor of q's dtype, device and shape")
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=device) if return_lse else None
-    scale = 1.0 / math.sqrt(d) if sm_scale is None else float(sm_scale)
-    with _on(device):
-        # from torch's allocator, so that calls on several streams and captured graphs have
-        # workspaces of their own
-        need = _lib.sa_cache_attn_workspace_bytes(T, args[3], H, Hq // H, d)
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        _check(_lib.sa_cache_attn(q.data_ptr(), o.data_ptr(), lse.data_ptr() if return_lse else None, _DTYPES[q.dtype],
-                                  T, stride, *args, Hq // H, d, bool(causal), min(int(window), 1 << 30), scale, ws.data_ptr(), need,
-                                  _raw_stream(device)), "sa_cache_attn")
-    return (o, lse) if return_lse else o
+    return _sa_torch.attn(*cache, q, tok_start, kv_lens, page_table, causal, window, sm_scale, return_lse, out)
 
 
 def sa_debug_qk_s32(q_i8, k_i8, N: int):

@@ -5,7 +5,9 @@
 Each ``csrc/*.cu`` file is compiled separately with nvcc for ``sm_100a`` (no fast-math:
 the prologue relies on IEEE division and round-to-nearest-even) and the objects are
 linked into ``bit_quantized_attention_sa_b200/libsa.so`` with the CUDA runtime linked
-statically, so the library loads next to any PyTorch build and from plain C.
+statically, so the library loads next to any PyTorch build and from plain C.  The torch side
+of the serving calls (``csrc/sa_torch.cpp``) becomes ``_sa_torch.so`` beside it, against the
+installed PyTorch.
 """
 from __future__ import annotations
 
@@ -30,6 +32,9 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=default",
     "-I", os.path.join(ROOT, "include"),
 ]
+
+
+TORCH_EXT = os.path.join(PKG, "_sa_torch.so")
 
 
 def nvcc() -> str:
@@ -61,7 +66,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-cudart", "static", "-o", LIB + ".tmp"] + objs
         subprocess.run(cmd, check=True)
         os.replace(LIB + ".tmp", LIB)
+    src = os.path.join(CSRC, "sa_torch.cpp")
+    if force or _stale(TORCH_EXT, [src, os.path.join(ROOT, "include", "sa.h"), __file__]):
+        build_torch_ext(src)
     return LIB
+
+
+def build_torch_ext(src: str) -> None:
+    """The torch side of the serving calls, _sa_torch.so, against libsa.so beside it and the
+    installed PyTorch (g++; no device code)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    dirs = include_paths() + [sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_sa_torch",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [x for d in dirs for x in ("-isystem", d)] + [src, "-o", TORCH_EXT + ".tmp"]
+    cmd += [f"-L{d}" for d in library_paths()] + [f"-L{PKG}", "-l:libsa.so", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                                                  "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    os.replace(TORCH_EXT + ".tmp", TORCH_EXT)
 
 
 def main(argv=None) -> int:

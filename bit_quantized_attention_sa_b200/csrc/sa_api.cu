@@ -3,6 +3,7 @@
 // stream.  No entry point synchronises except sa_get_device_status and
 // sa_release_workspace.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -69,6 +70,18 @@ bool encode_tmap_3d_f32(CUtensorMap *map, const void *base, uint64_t d0, uint64_
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The current device's SM count (0: no device), asked for once per device.
+int device_sms()
+{
+    static std::atomic<int> cached[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64 && (sms = cached[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) cached[dev].store(sms, std::memory_order_relaxed);
+    return sms;
 }
 
 // ------------------------------------------------------------------ validation
@@ -445,15 +458,6 @@ static sa_status check_tokens(const void *p, int64_t stride, int64_t width)
     if (!p || stride < width) return SA_ERR_INVALID_ARG;
     if (!aligned16(p) || stride % 8 != 0) return SA_ERR_MISALIGNED;
     return SA_OK;
-}
-
-static int device_sms()
-{
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
 }
 
 }  // namespace sa

@@ -584,13 +584,6 @@ cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const C
     return cudaGetLastError();
 }
 
-cudaError_t sm_count(int *sms)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
-}
-
 size_t meta_bytes(int sms) { return (size_t(workers_of(sms)) * sizeof(int4) + 255) & ~size_t(255); }
 
 }  // namespace
@@ -604,9 +597,9 @@ size_t cache_attn_workspace(int sms, int d)
 cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
                               cudaStream_t st)
 {
-    int sms = 0;
-    cudaError_t e = sm_count(&sms);
-    if (e != cudaSuccess) return e;
+    const int sms = device_sms();
+    if (sms < 1) return cudaErrorNoDevice;
+    cudaError_t e = cudaSuccess;
     a.meta = static_cast<int4 *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + meta_bytes(sms));
     if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) {

@@ -108,6 +108,7 @@ cudaError_t launch_sla_linear(const void *q, const void *k, const void *v, const
 // keep[e] = classes[e] >= 2 (the sparse part's block mask), n entries.
 cudaError_t launch_sla_critical(const uint8_t *classes, int64_t n, uint8_t *keep, cudaStream_t st);
 cudaError_t read_and_clear_sla_status(int *status);
+int device_sms();  // of the current device (sa_api.cu)
 // ---- rotary positions (sa_rope.cu)
 struct RopeIo {
     const void *x = nullptr;

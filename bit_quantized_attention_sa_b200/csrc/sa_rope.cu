@@ -191,10 +191,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A)
 
 cudaError_t launch_rope(RopeArgs a, int dtype, cudaStream_t st)
 {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    const int sms = device_sms();
     const int units = a.d / 16, heads = a.io[0].heads + a.io[1].heads;
     a.tile_tokens = units <= 8 ? 8 : kTileUnits / units;
     const int slots = kThreads / (a.tile_tokens * units);

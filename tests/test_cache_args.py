@@ -69,13 +69,18 @@ def test_attn_workspace_of_refused_sizes_is_zero(libsa):
     assert f(1, 0, 8, 1, 128) == 0 and f(1, 1, 8, 1, 96) == 0 and f(1, 1, 8, 0, 128) == 0 and f(-1, 1, 8, 1, 128) == 0
 
 
-def _rope(lib, libsa, **kw):
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("x_batch", "x_head", "x_tok", "y_batch", "y_head", "y_tok")] + [("heads", ctypes.c_int)]
+
+
+def _rope(lib, **kw):
     a = dict(count=1, dtype=0, B=1, N=8, d=128, rot=128, inter=0, pos=FAKE, pa=0, pb=0, axes=1, sections=None, freqs=FAKE,
              amp=ctypes.c_float(1.0), inverse=0)
     t = dict(x=FAKE, y=FAKE, x_batch=0, x_head=1024, x_tok=128, y_batch=0, y_head=1024, y_tok=128, heads=4)
     t.update({k: kw.pop(k) for k in list(kw) if k in t})
     a.update(kw)
-    arr = (libsa._RopeTensor * 2)(libsa._RopeTensor(**t), libsa._RopeTensor(**t))
+    arr = (RopeTensor * 2)(RopeTensor(**t), RopeTensor(**t))
     return lib.sa_rope(arr, *a.values(), None)
 
 
@@ -88,7 +93,7 @@ def _rope(lib, libsa, **kw):
     (dict(x_tok=132), 3), (dict(freqs=FAKE + 4), 3), (dict(pos=FAKE + 2), 3), (dict(N=0, x=None), 0), (dict(B=0), 0),
 ])
 def test_rope_refusals(libsa, kw, expect):
-    assert _rope(libsa.raw_library(), libsa, **kw) == expect
+    assert _rope(libsa.raw_library(), **kw) == expect
 
 
 def test_binding_refusals(libsa):
