@@ -1,7 +1,8 @@
 // sa_cache_attn.cu -- attention of few query rows over the paged INT8 cache for sm_100a.
 //
 // Rows of a (sequence, key/value head) are its query tokens times the query heads that share
-// the head, token-major; a tile is 16 rows, the M of one mma.  For every 64-token block j
+// the head, token-major; a tile is 8 rows, the N of one mma (the codes are its M, so that few
+// rows waste little), and a warp works on one or two tiles.  For every 64-token block j
 //     S = q . k8,   x = S * (scale_k[j] * sm_scale),   p = exp(x - m),
 //     acc = acc * alpha + (p * scale_v[j]) . v8,   l = l * alpha + sum p,
 // with m, l and acc in fp32; in the end o = acc / l and lse = m + log l.
@@ -38,24 +39,27 @@ __device__ int g_cache_attn_status;  // 0 = OK, 6 = a bounded wait expired, 8 = 
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;         // rows of a tile
 // Rows of a sequence and head, on average, up to which this kernel takes a call; the others go
 // to the tensor-core kernel of sa_cache_chunk.cu.
 constexpr int kFewRows = 32;
-constexpr int kSlots = 3;         // ring slots of a warp, one K or V tile each
 constexpr float kPScale = 16384.0f;
 
-template <int D>
+// D: head size; NT: tiles of eight rows that a warp works on at once.  One tile leaves registers
+// for twelve warps, with a ring of two slots (a K or V tile of 64 x D bytes each); two tiles for
+// eight warps with three.
+template <int D, int NT>
 struct Sizes {
-    static constexpr uint32_t kTile = 64 * D;  // bytes of a K or V tile
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kWarps = NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
+    static constexpr int kSlots = NT == 1 ? 2 : 3;
+    static constexpr uint32_t kTile = 64 * D;
     static constexpr uint32_t kOffBar = kWarps * kSlots * kTile;
     static constexpr uint32_t kBytes = kOffBar + kWarps * kSlots * 8;
     static constexpr uint32_t kAlloc = kBytes + 1024;
     static constexpr int kPart = kRows * (D + 2);  // floats of a partial result
 };
-static_assert(Sizes<128>::kAlloc <= 227 * 1024, "shared memory per CTA");
+static_assert(Sizes<128, 1>::kAlloc <= 220 * 1024 && Sizes<128, 2>::kAlloc <= 220 * 1024, "shared memory per CTA");
+constexpr int kMaxWarps = 12;
 
 __device__ __forceinline__ void record(int what) { atomicMax(&g_cache_attn_status, what); }
 
@@ -67,14 +71,22 @@ struct Seq {
     __device__ int64_t blocks(int heads) const { return int64_t(heads) * tiles * nb; }
 };
 
-__device__ __forceinline__ Seq load_seq(const CacheAttnArgs &A, int b)
+__device__ __forceinline__ Seq load_seq(const CacheAttnArgs &A, int b, int rows)
 {
     Seq s;
     if (!load_span(A, b, s.ts, s.n, s.len)) record(8);
-    s.tiles = (s.n * A.G + kRows - 1) / kRows;
+    s.tiles = (s.n * A.G + rows - 1) / rows;
     s.lo = A.window > 0 ? max(0, s.len - s.n - A.window + 1) / kPage : 0;
     s.nb = max(1, (s.len + kPage - 1) / kPage - s.lo);
     return s;
+}
+
+// An 8 x 8 matrix of 16-bit values, two of a row in each lane, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -91,15 +103,16 @@ struct Entry {
     float sk, sv;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const CacheAttnArgs A)
 {
-    using S = Sizes<D>;
-    constexpr int kSteps = D / 16;   // k16 steps of q . k
+    using S = Sizes<D, NT>;
+    constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kSlots = S::kSlots, kRows = S::kRows;
+    constexpr int kSteps = D / 16;   // k16 steps of k8 . q
     constexpr int kQuads = D / 64;   // 16-byte chunks of a key row that a lane reads
-    constexpr int kNT = D / 8;       // n8 tiles of acc
+    constexpr int kMT = D / 16;      // 16-channel tiles of acc
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int64_t prefix[kThreads + 1];
@@ -113,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t mine = 0;
     for (int i = 0; i < per; ++i) {
         const int b = int(threadIdx.x) * per + i;
-        if (b < A.B) mine += load_seq(A, b).blocks(A.H);
+        if (b < A.B) mine += load_seq(A, b, S::kRows).blocks(A.H);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -160,13 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         cb = (t - 1) * per;  // threads without sequences share the last prefix: still its end
         cbase = prefix[t - 1];
     }
-    Seq cs = load_seq(A, min(cb, A.B - 1));
+    Seq cs = load_seq(A, min(cb, A.B - 1), S::kRows);
     auto next_entry = [&](int64_t f) -> Entry {
         Entry e;
         while (cb < A.B && f >= cbase + cs.blocks(A.H)) {
             cbase += cs.blocks(A.H);
             ++cb;
-            if (cb < A.B) cs = load_seq(A, cb);
+            if (cb < A.B) cs = load_seq(A, cb, S::kRows);
         }
         e.b = cb;
         e.seg = 0;
@@ -219,12 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool split = false;               // this worker began a segment that goes on elsewhere
     Seq sq{};
     int head = 0, row0 = 0, tile_first = 0, tile_last = -1, all_first = 0, all_last = -1;
-    uint32_t qf[kSteps][4];
-    float row_c[2], m[2], l[2], acc[kNT][4], u_ref = 0.0f;
-    int row_first[2], row_last[2];
+    uint32_t qf[NT][kSteps][2];
+    float row_c[NT][2], m[NT][2], l[NT][2], acc[NT][kMT][4], u_ref = 0.0f;
+    int row_first[NT][2], row_last[NT][2];
 
     auto open_segment = [&](int b, int sg) {
-        if (b != seg_b) sq = load_seq(A, b);
+        if (b != seg_b) sq = load_seq(A, b, kRows);
         head = sg / sq.tiles;
         row0 = (sg - head * sq.tiles) * kRows;
         const int rows = sq.n * A.G, pos0 = sq.len - sq.n;
@@ -236,14 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         all_last = last_of(i_lo);
         tile_last = last_of(i_hi);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int rr = row0 + g + 8 * r, i = rr / A.G;
+        for (int n = 0; n < NT; ++n) {
+            // this lane reads 16 channels (or 32) of row g; it holds the statistics of rows 2c, 2c + 1
+            const int rr = row0 + 8 * n + g, i = rr / A.G;
             const bool valid = rr < rows;
-            row_first[r] = first_of(i);
-            row_last[r] = valid ? last_of(i) : -1;
-            float x[kQuads][16], top = 0.0f;
             const T *src = static_cast<const T *>(A.q) + (int64_t(sq.ts) + i) * A.q_stride +
                            int64_t(head * A.G + rr - i * A.G) * D;
+            float x[kQuads][16], top = 0.0f;
 #pragma unroll
             for (int j = 0; j < kQuads; ++j)
 #pragma unroll
@@ -262,20 +274,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 row_power(top, up, down);
             }
-            row_c[r] = A.sm_scale * kLog2e * down;
 #pragma unroll
             for (int j = 0; j < kQuads; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float *f = &x[j][4 * k];
-                    qf[4 * j + k][r] = h2(__floats2half2_rn(f[0] * up, f[1] * up));
-                    qf[4 * j + k][2 + r] = h2(__floats2half2_rn(f[2] * up, f[3] * up));
+                    qf[n][4 * j + k][0] = h2(__floats2half2_rn(f[0] * up, f[1] * up));
+                    qf[n][4 * j + k][1] = h2(__floats2half2_rn(f[2] * up, f[3] * up));
                 }
-            m[r] = -INFINITY;
-            l[r] = 0.0f;
-        }
 #pragma unroll
-        for (int i = 0; i < kNT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+            for (int e = 0; e < 2; ++e) {
+                row_c[n][e] = A.sm_scale * kLog2e * __shfl_sync(0xffffffffu, down, 4 * (2 * c + e));
+                const int rs = row0 + 8 * n + 2 * c + e, is = rs / A.G;
+                row_first[n][e] = first_of(is);
+                row_last[n][e] = rs < rows ? last_of(is) : -1;
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kMT; ++k) acc[n][k][0] = acc[n][k][1] = acc[n][k][2] = acc[n][k][3] = 0.0f;
+        }
         u_ref = 0.0f;
     };
 
@@ -290,48 +308,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             split = true;
             if (lane == 0) A.meta[w] = make_int4(seg_b, seg, int((seg_end - 1) / chunk), slot);
         }
+        // the lane's channels: 16 (or 8) from ch on, of rows 2c and 2c + 1
+        const int ch = D == 128 ? 16 * ((g & 1) * 4 + (g >> 1)) : 8 * g;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            const int rt = g + 8 * r;
-            if (rt >= rows) continue;
-            if (whole) {
-                const float f = l[r] == 0.0f ? 0.0f : u_ref / (kPScale * l[r]);
-                const int rr = row0 + rt, i = rr / A.G, hq = head * A.G + rr - i * A.G;
-                const int64_t at = (int64_t(sq.ts) + i) * (A.H * A.G) + hq;
-                T *dst = static_cast<T *>(A.o) + at * D;
-                if (A.lse && c == 0) A.lse[at] = l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int ch = D == 128 ? 16 * (c + 4 * e) : 16 * c + 8 * e;
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[n][e];
 #pragma unroll
-                    for (int i8 = 0; i8 < kNT; i8 += 8) {
-                        uint32_t p[4];
+                for (int o = 4; o < 32; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const int rt = 8 * n + 2 * c + e;
+                if (rt >= rows) continue;
+                if (whole) {
+                    const float f = sum == 0.0f ? 0.0f : u_ref / (kPScale * sum);
+                    const int rr = row0 + rt, i = rr / A.G, hq = head * A.G + rr - i * A.G;
+                    const int64_t at = (int64_t(sq.ts) + i) * (A.H * A.G) + hq;
+                    T *dst = static_cast<T *>(A.o) + at * D + ch;
+                    if (A.lse && g == 0) A.lse[at] = sum == 0.0f ? -INFINITY : (m[n][e] + log2f(sum)) * kLn2;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            p[k] = pack_out(acc[i8 + 2 * k][2 * r + e] * f, acc[i8 + 2 * k + 1][2 * r + e] * f, T());
-                        *reinterpret_cast<uint4 *>(dst + ch + i8) = make_uint4(p[0], p[1], p[2], p[3]);
+                    for (int k = 0; k < kMT; k += 4)
+                        *reinterpret_cast<uint4 *>(dst + 2 * k) =
+                            make_uint4(pack_out(acc[n][k][e] * f, acc[n][k][2 + e] * f, T()),
+                                       pack_out(acc[n][k + 1][e] * f, acc[n][k + 1][2 + e] * f, T()),
+                                       pack_out(acc[n][k + 2][e] * f, acc[n][k + 2][2 + e] * f, T()),
+                                       pack_out(acc[n][k + 3][e] * f, acc[n][k + 3][2 + e] * f, T()));
+                } else {
+                    float *part = A.part + int64_t(slot) * S::kPart;
+                    if (g == 0) {
+                        part[kRows * D + rt] = m[n][e];
+                        part[kRows * (D + 1) + rt] = sum;
                     }
-                }
-            } else {
-                float *part = A.part + int64_t(slot) * S::kPart;
-                if (c == 0) {
-                    part[kRows * D + rt] = m[r];
-                    part[kRows * D + kRows + rt] = l[r];
-                }
-                const float f = u_ref * (1.0f / kPScale);
+                    const float f = u_ref * (1.0f / kPScale);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int ch = D == 128 ? 16 * (c + 4 * e) : 16 * c + 8 * e;
-#pragma unroll
-                    for (int k = 0; k < kNT; k += 4)
-                        *reinterpret_cast<float4 *>(part + rt * D + ch + k) =
-                            make_float4(acc[k][2 * r + e] * f, acc[k + 1][2 * r + e] * f, acc[k + 2][2 * r + e] * f,
-                                        acc[k + 3][2 * r + e] * f);
+                    for (int k = 0; k < kMT; k += 2)
+                        *reinterpret_cast<float4 *>(part + rt * D + ch + 2 * k) =
+                            make_float4(acc[n][k][e] * f, acc[n][k][2 + e] * f, acc[n][k + 1][e] * f, acc[n][k + 1][2 + e] * f);
                 }
             }
-        }
     };
 
     for (int i = 0; i < count; ++i) {
@@ -356,26 +369,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool seen = t0 <= tile_last && t0 + kPage > tile_first;
         const bool full = t0 >= all_first && t0 + kPage - 1 <= all_last;
 
-        // ---- S = q . k8
+        // ---- S^T = k8 . q: 16 keys by 8 rows a product
         ok = mbar_wait(bars + 8 * uint32_t(done % kSlots), uint32_t(done / kSlots) & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        float s[8][4];
+        float s[NT][4][4];
         if (seen) {
             const uint8_t *tile = ring + (done % kSlots) * S::kTile;
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-                const int key = 8 * nt + (D == 128 ? (g & 1) * 4 + (g >> 1) : g);
+            for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[n][mt][0] = s[n][mt][1] = s[n][mt][2] = s[n][mt][3] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < kQuads; ++j) {
-                    const int chunk16 = D == 128 ? c + 4 * j : (key & 1) * 4 + c;
-                    const int ln = D == 128 ? key : key >> 1;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + ln * 128 + ((chunk16 ^ (ln & 7)) << 4));
-                    const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+                    uint4 v[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int key = 16 * mt + 8 * y + (D == 128 ? (g & 1) * 4 + (g >> 1) : g);
+                        const int chunk16 = D == 128 ? c + 4 * j : (key & 1) * 4 + c;
+                        const int ln = D == 128 ? key : key >> 1;
+                        v[y] = *reinterpret_cast<const uint4 *>(tile + ln * 128 + ((chunk16 ^ (ln & 7)) << 4));
+                    }
+                    const uint32_t w0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, w1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t u8 = wd[k] ^ 0x80808080u;
-                        mma16816(s[nt], qf[4 * j + k], bytes_to_h2(u8, 0x4140u), bytes_to_h2(u8, 0x4342u));
+                        const uint32_t x0 = w0[k] ^ 0x80808080u, x1 = w1[k] ^ 0x80808080u;
+                        const uint32_t a[4] = {bytes_to_h2(x0, 0x4140u), bytes_to_h2(x1, 0x4140u), bytes_to_h2(x0, 0x4342u),
+                                               bytes_to_h2(x1, 0x4342u)};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816(s[n][mt], a, qf[n][4 * j + k][0], qf[n][4 * j + k][1]);
                     }
                 }
             }
@@ -384,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue(done + kSlots, window);
         ++done;
 
-        // ---- p = exp(x - m), in powers of two
-        uint32_t pf[8][2];
+        // ---- p = exp(x - m), in powers of two; pf: P as the second operand, 8 keys by 8 rows each
+        uint32_t pf[NT][8];
         if (seen) {
             float ratio, su = 1.0f;
             if (sv >= 2.0f * u_ref && sv > 0.0f && sv < INFINITY) {
@@ -394,65 +415,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u_ref = u_new;
             }
             ratio = sv == 0.0f ? 0.0f : kPScale * (sv / u_ref);
-            float factor[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float sc = row_c[r] * sk;
-                float top = -INFINITY;
+            for (int n = 0; n < NT; ++n) {
+                float factor[2], ref[2], top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
+                for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = s[nt][2 * r + e] * sc;
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[n][mt][e] * (row_c[n][e & 1] * sk);
                         if (!full) {
-                            const int t = t0 + 8 * nt + (D == 128 ? c + 4 * e : 2 * c + e);
-                            if (t < row_first[r] || t > row_last[r]) x = -INFINITY;
+                            const int t = t0 + 16 * mt + 8 * (e >> 1) + (D == 128 ? (g & 1) * 4 + (g >> 1) : g);
+                            if (t < row_first[n][e & 1] || t > row_last[n][e & 1]) x = -INFINITY;
                         }
-                        s[nt][2 * r + e] = x;
-                        top = fmaxf(top, x);
+                        s[n][mt][e] = x;
+                        top[e & 1] = fmaxf(top[e & 1], x);
                     }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float m_new = fmaxf(m[r], top);
-                const float ref = m_new == -INFINITY ? 0.0f : m_new;
-                const float alpha = ex2_approx(m[r] - ref);
-                float sum = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                    float p[2], y[2];
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = s[nt][2 * r + e];
-                        p[e] = ex2_approx(x - ref);
-                        y[e] = p[e] * ratio;
-                        if (!full && x == -INFINITY) y[e] = 0.0f;  // whatever the block's scale
-                    }
-                    sum += p[0] + p[1];
-                    pf[nt][r] = h2(__floats2half2_rn(y[0], y[1]));
+                    for (int o = 4; o < 32; o *= 2) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+                    const float m_new = fmaxf(m[n][e], top[e]);
+                    ref[e] = m_new == -INFINITY ? 0.0f : m_new;
+                    const float alpha = ex2_approx(m[n][e] - ref[e]);
+                    l[n][e] *= alpha;
+                    m[n][e] = m_new;
+                    factor[e] = alpha * su;
                 }
-                l[r] = l[r] * alpha + sum;
-                m[r] = m_new;
-                factor[r] = alpha * su;
-            }
-            if (__any_sync(0xffffffffu, factor[0] != 1.0f || factor[1] != 1.0f)) {
 #pragma unroll
-                for (int k = 0; k < kNT; ++k) {
-                    acc[k][0] *= factor[0];
-                    acc[k][1] *= factor[0];
-                    acc[k][2] *= factor[1];
-                    acc[k][3] *= factor[1];
+                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float z[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = s[n][mt][2 * y + e], p = ex2_approx(x - ref[e]);
+                            l[n][e] += p;
+                            z[e] = p * ratio;
+                            if (!full && x == -INFINITY) z[e] = 0.0f;  // whatever the block's scale
+                        }
+                        pf[n][2 * mt + y] = transpose8x8(h2(__floats2half2_rn(z[0], z[1])));
+                    }
+                if (__any_sync(0xffffffffu, factor[0] != 1.0f || factor[1] != 1.0f)) {
+#pragma unroll
+                    for (int k = 0; k < kMT; ++k) {
+                        acc[n][k][0] *= factor[0];
+                        acc[n][k][1] *= factor[1];
+                        acc[n][k][2] *= factor[0];
+                        acc[n][k][3] *= factor[1];
+                    }
                 }
             }
         }
 
-        // ---- acc += p . v8
+        // ---- acc^T += v8^T . P^T: 16 channels by 8 rows a product
         ok = mbar_wait(bars + 8 * uint32_t(done % kSlots), uint32_t(done / kSlots) & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         if (seen) {
             const uint8_t *tile = ring + (done % kSlots) * S::kTile;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {  // 16 keys
-                uint32_t vw[4][kNT / 4];      // 4 keys x kNT channels of this lane
+                uint32_t vw[4][D / 32];       // 4 keys x D / 8 channels of this lane
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const int in8 = D == 128 ? c + 4 * (y & 1) : 2 * c + (y & 1);
@@ -463,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<const uint4 *>(tile + key * 128 + ((chunk16 ^ (key & 7)) << 4));
                         vw[y][0] = v.x;
                         vw[y][1] = v.y;
-                        vw[y][kNT / 4 - 2] = v.z;
-                        vw[y][kNT / 4 - 1] = v.w;
+                        vw[y][D / 32 - 2] = v.z;
+                        vw[y][D / 32 - 1] = v.w;
                     } else {
                         const int ln = key >> 1, chunk16 = (key & 1) * 4 + (g >> 1);
                         const uint2 v = *reinterpret_cast<const uint2 *>(
@@ -473,9 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         vw[y][1] = v.y;
                     }
                 }
-                const uint32_t a[4] = {pf[2 * kk][0], pf[2 * kk][1], pf[2 * kk + 1][0], pf[2 * kk + 1][1]};
 #pragma unroll
-                for (int q4 = 0; q4 < kNT / 4; ++q4) {
+                for (int q4 = 0; q4 < D / 32; ++q4) {
                     uint32_t lo[2], hi[2];  // channels 4 q4 + {0, 1}, {2, 3} of both key pairs
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
@@ -483,10 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lo[y] = __byte_perm(w0, w1, 0x5140) ^ 0x80808080u;
                         hi[y] = __byte_perm(w0, w1, 0x7362) ^ 0x80808080u;
                     }
-                    mma16816(acc[4 * q4], a, bytes_to_h2(lo[0], 0x4140u), bytes_to_h2(lo[1], 0x4140u));
-                    mma16816(acc[4 * q4 + 1], a, bytes_to_h2(lo[0], 0x4342u), bytes_to_h2(lo[1], 0x4342u));
-                    mma16816(acc[4 * q4 + 2], a, bytes_to_h2(hi[0], 0x4140u), bytes_to_h2(hi[1], 0x4140u));
-                    mma16816(acc[4 * q4 + 3], a, bytes_to_h2(hi[0], 0x4342u), bytes_to_h2(hi[1], 0x4342u));
+                    const uint32_t a[4] = {bytes_to_h2(lo[0], 0x4140u), bytes_to_h2(lo[0], 0x4342u), bytes_to_h2(lo[1], 0x4140u),
+                                           bytes_to_h2(lo[1], 0x4342u)};
+                    const uint32_t b4[4] = {bytes_to_h2(hi[0], 0x4140u), bytes_to_h2(hi[0], 0x4342u), bytes_to_h2(hi[1], 0x4140u),
+                                            bytes_to_h2(hi[1], 0x4342u)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816(acc[n][2 * q4], a, pf[n][2 * kk], pf[n][2 * kk + 1]);
+                        mma16816(acc[n][2 * q4 + 1], b4, pf[n][2 * kk], pf[n][2 * kk + 1]);
+                    }
                 }
             }
         }
@@ -507,12 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the segment, of ROWS rows at most, that worker blockIdx.x began and others
-// went on with, 16 rows (blockIdx.y) a block.  A piece is acc [ROWS][D], m [ROWS], l [ROWS].
+// went on with, 16 rows (blockIdx.y) a block.  A piece is acc [ROWS][D], m [ROWS], l [ROWS].  The
+// warps take the rows, and share a row's pieces where there are fewer rows.
+constexpr int kCombineWarps = 16, kCombineThreads = 32 * kCombineWarps;
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) cache_combine_kernel(const CacheAttnArgs A)
+__global__ void __launch_bounds__(kCombineThreads) cache_combine_kernel(const CacheAttnArgs A)
 {
     constexpr int kPart = ROWS * (D + 2), kPer = D / 32;
-    __shared__ float sums[kWarps][D];
+    __shared__ float sums[kCombineWarps][D];
+    cudaGridDependencySynchronize();  // launched early: the pieces are there from here on
     const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 meta = A.meta[w];
     if (meta.z <= w) return;
@@ -520,78 +549,108 @@ __global__ void __launch_bounds__(kThreads) cache_combine_kernel(const CacheAttn
     if (!load_span(A, meta.x, ts, n, len)) return;
     const int tiles = (n * A.G + ROWS - 1) / ROWS;
     const int head = meta.y / tiles, row0 = (meta.y - head * tiles) * ROWS + 16 * int(blockIdx.y);
-    const int rows = min(16, n * A.G - row0), pieces = meta.z - w + 1;
+    const int rows = min(ROWS < 16 ? ROWS : 16, n * A.G - row0), pieces = meta.z - w + 1;
     if (rows <= 0) return;
     int groups = 1;
-    while (groups < rows && groups < kWarps) groups *= 2;
-    const int subs = kWarps / groups, sub = warp / groups;
+    while (groups < rows) groups *= 2;
+    const int subs = kCombineWarps / groups, sub = warp / groups, r = warp % groups, rp = r + 16 * int(blockIdx.y);
     auto part_of = [&](int p) { return A.part + int64_t(p == 0 ? meta.w : 2 * (w + p)) * kPart; };
-    for (int r0 = 0; r0 < rows; r0 += groups) {
-        const int r = r0 + warp % groups, rp = r + 16 * int(blockIdx.y);
-        float big = -INFINITY, total = 0.0f, out[kPer];
+    float big = -INFINITY, total = 0.0f, out[kPer];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) out[k] = 0.0f;
-        if (r < rows) {
-            for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + rp]);
+    for (int k = 0; k < kPer; ++k) out[k] = 0.0f;
+    if (r < rows) {
+        for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + rp]);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const float ref = big == -INFINITY ? 0.0f : big;
-            for (int p = lane; p < pieces; p += 32) {
-                const float *part = part_of(p);
-                total += ex2_approx(part[ROWS * D + rp] - ref) * part[ROWS * (D + 1) + rp];
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-#pragma unroll 4
-            for (int p = sub; p < pieces; p += subs) {
-                const float *part = part_of(p);
-                const float f = ex2_approx(part[ROWS * D + rp] - ref);
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) out[k] += f * part[rp * D + lane + 32 * k];
-            }
+        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        const float ref = big == -INFINITY ? 0.0f : big;
+        for (int p = lane; p < pieces; p += 32) {
+            const float *part = part_of(p);
+            total += ex2_approx(part[ROWS * D + rp] - ref) * part[ROWS * (D + 1) + rp];
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll 8
+        for (int p = sub; p < pieces; p += subs) {
+            const float *part = part_of(p);
+            const float f = ex2_approx(part[ROWS * D + rp] - ref);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) out[k] += f * part[rp * D + lane + 32 * k];
+        }
+    }
+    if (subs > 1) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) sums[warp][lane + 32 * k] = out[k];
         __syncthreads();
-        if (sub == 0 && r < rows) {
-            const float f = total == 0.0f ? 0.0f : 1.0f / total;
-            const int rr = row0 + r, i = rr / A.G;
-            const int64_t at = (int64_t(ts) + i) * (A.H * A.G) + head * A.G + rr - i * A.G;
+        if (sub > 0) return;
+        for (int y = 1; y < subs; ++y)
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                float x = 0.0f;
-                for (int y = 0; y < subs; ++y) x += sums[warp + y * groups][lane + 32 * k];
-                const uint32_t p = pack_out(x * f, 0.0f, T());
-                static_cast<uint16_t *>(A.o)[at * D + lane + 32 * k] = uint16_t(p);
-            }
-            if (A.lse && lane == 0) A.lse[at] = total == 0.0f ? -INFINITY : (big + log2f(total)) * kLn2;
-        }
-        __syncthreads();
+            for (int k = 0; k < kPer; ++k) out[k] += sums[warp + y * groups][lane + 32 * k];
     }
+    if (r >= rows) return;
+    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+    const int rr = row0 + r, i = rr / A.G;
+    const int64_t at = (int64_t(ts) + i) * (A.H * A.G) + head * A.G + rr - i * A.G;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        static_cast<uint16_t *>(A.o)[at * D + lane + 32 * k] = uint16_t(pack_out(out[k] * f, 0.0f, T()));
+    if (A.lse && lane == 0) A.lse[at] = total == 0.0f ? -INFINITY : (big + log2f(total)) * kLn2;
 }
 
-int workers_of(int sms) { return sms * kWarps; }
+// The combine kernel is launched while the kernel before it still runs (it waits for its end on
+// the device), which hides its launch.
+template <typename T, int D, int ROWS>
+cudaError_t launch_combine(const CacheAttnArgs &a, int workers, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(workers), ROWS <= 16 ? 1 : ROWS / 16);
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_combine_kernel<T, D, ROWS>, a);
+}
 
-template <typename T, int D>
+template <typename T, int D, int NT>
 cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms, cudaStream_t st)
 {
-    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(Sizes<D>::kAlloc));
+    using S = Sizes<D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(S::kAlloc));
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<T, D><<<sms, kThreads, Sizes<D>::kAlloc, st>>>(tm_k, tm_v, a);
+    cache_attn_kernel<T, D, NT><<<sms, S::kThreads, S::kAlloc, st>>>(tm_k, tm_v, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cache_combine_kernel<T, D, kRows><<<workers_of(sms), kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_combine<T, D, S::kRows>(a, sms * S::kWarps, st);
 }
 
-size_t meta_bytes(int sms) { return (size_t(workers_of(sms)) * sizeof(int4) + 255) & ~size_t(255); }
+template <typename T, int D>
+cudaError_t launch_any(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms, cudaStream_t st)
+{
+    if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) {
+        const cudaError_t e = launch_cache_chunk(a, sms, st);
+        return e == cudaSuccess ? launch_combine<T, D, 256>(a, sms, st) : e;
+    }
+    // two tiles of eight rows at once where most segments have more than eight
+    if (int64_t(a.T) * a.G > int64_t(8) * a.B) return launch_for<T, D, 2>(tm_k, tm_v, a, sms, st);
+    return launch_for<T, D, 1>(tm_k, tm_v, a, sms, st);
+}
+
+size_t meta_bytes(int sms) { return (size_t(sms) * kMaxWarps * sizeof(int4) + 255) & ~size_t(255); }
+
+template <int D>
+size_t part_bytes(int sms)
+{
+    const size_t one = size_t(Sizes<D, 1>::kWarps) * Sizes<D, 1>::kPart, two = size_t(Sizes<D, 2>::kWarps) * Sizes<D, 2>::kPart;
+    return std::max(size_t(2) * sms * std::max(one, two) * 4, cache_chunk_part_bytes(sms, D));
+}
 
 }  // namespace
 
 size_t cache_attn_workspace(int sms, int d)
 {
-    const size_t few = size_t(2) * workers_of(sms) * size_t(d == 128 ? Sizes<128>::kPart : Sizes<64>::kPart) * 4;
-    return meta_bytes(sms) + std::max(few, cache_chunk_part_bytes(sms, d));
+    return meta_bytes(sms) + (d == 128 ? part_bytes<128>(sms) : part_bytes<64>(sms));
 }
 
 cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
@@ -599,26 +658,12 @@ cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, 
 {
     const int sms = device_sms();
     if (sms < 1) return cudaErrorNoDevice;
-    cudaError_t e = cudaSuccess;
     a.meta = static_cast<int4 *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + meta_bytes(sms));
-    if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) {
-        if ((e = launch_cache_chunk(a, sms, st)) != cudaSuccess) return e;
-        const dim3 grid(unsigned(sms), 16);
-        if (a.dtype == 0 && a.d == 128)
-            cache_combine_kernel<__nv_bfloat16, 128, 256><<<grid, kThreads, 0, st>>>(a);
-        else if (a.dtype == 0)
-            cache_combine_kernel<__nv_bfloat16, 64, 256><<<grid, kThreads, 0, st>>>(a);
-        else if (a.d == 128)
-            cache_combine_kernel<__half, 128, 256><<<grid, kThreads, 0, st>>>(a);
-        else
-            cache_combine_kernel<__half, 64, 256><<<grid, kThreads, 0, st>>>(a);
-        return cudaGetLastError();
-    }
     if (a.dtype == 0)
-        return a.d == 128 ? launch_for<__nv_bfloat16, 128>(tm_k, tm_v, a, sms, st)
-                          : launch_for<__nv_bfloat16, 64>(tm_k, tm_v, a, sms, st);
-    return a.d == 128 ? launch_for<__half, 128>(tm_k, tm_v, a, sms, st) : launch_for<__half, 64>(tm_k, tm_v, a, sms, st);
+        return a.d == 128 ? launch_any<__nv_bfloat16, 128>(tm_k, tm_v, a, sms, st)
+                          : launch_any<__nv_bfloat16, 64>(tm_k, tm_v, a, sms, st);
+    return a.d == 128 ? launch_any<__half, 128>(tm_k, tm_v, a, sms, st) : launch_any<__half, 64>(tm_k, tm_v, a, sms, st);
 }
 
 cudaError_t read_and_clear_cache_attn_status(int *status)
