@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
     const int64_t start = w * chunk;
     const int count = int(max(int64_t(0), min(total, start + chunk) - start));
     if (count == 0) {
-        if (lane == 0) A.meta[w] = make_int4(0, 0, 0, 0);
+        if (lane == 0) A.meta[2 * w] = make_int4(0, 0, 0, 0);
         return;
     }
 
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         }
         return e;
     };
-    Entry cur = next_entry(start + lane), nxt = next_entry(start + 32 + lane);
+    Entry cur = next_entry(start + lane), nxt = cur;
 
     // tile u of the worker (u = 2 * block + (0 K, 1 V)) goes to slot u % kSlots
     auto issue = [&](int u, int first) {
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
     };
     __syncwarp();
     for (int u = 0; u < kSlots; ++u) issue(u, 0);
+    if (count > 32 - kSlots) nxt = next_entry(start + 32 + lane);
 
     // The reads of a tile are over before TMA writes its slot again: without the proxy fence a read
     // still in flight can be overtaken.
@@ -306,7 +307,10 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         const int slot = 2 * w + (seg_i == 0 ? 0 : 1);
         if (begins && !whole) {
             split = true;
-            if (lane == 0) A.meta[w] = make_int4(seg_b, seg, int((seg_end - 1) / chunk), slot);
+            if (lane == 0) {
+                A.meta[2 * w] = make_int4(int((seg_end - 1) / chunk) - w + 1, slot, 0, 0);
+                A.meta[2 * w + 1] = make_int4(sq.ts, head, row0, min(kRows, rows));
+            }
         }
         // the lane's channels: 16 (or 8) from ch on, of rows 2c and 2c + 1
         const int ch = D == 128 ? 16 * ((g & 1) * 4 + (g >> 1)) : 8 * g;
@@ -529,80 +533,123 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
             for (int i = 0; i < 1 << 20 && !mbar_try_wait(bars + 8 * uint32_t(u % kSlots), uint32_t(u / kSlots) & 1u); ++i) {
             }
     }
-    if (!split && lane == 0) A.meta[w] = make_int4(0, 0, 0, 0);
+    if (!split && lane == 0) A.meta[2 * w] = make_int4(0, 0, 0, 0);
 }
 
-// Joins the pieces of the segment, of ROWS rows at most, that worker blockIdx.x began and others
-// went on with, 16 rows (blockIdx.y) a block.  A piece is acc [ROWS][D], m [ROWS], l [ROWS].  The
-// warps take the rows, and share a row's pieces where there are fewer rows.
-constexpr int kCombineWarps = 16, kCombineThreads = 32 * kCombineWarps;
+__device__ __forceinline__ void load_floats(const float *p, float (&v)[4])
+{
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void load_floats(const float *p, float (&v)[2])
+{
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    v[0] = x.x; v[1] = x.y;
+}
+
+// Joins the pieces of the segments, of ROWS rows at most, that a worker began and others went on
+// with: workers blockIdx.x, blockIdx.x + gridDim.x, ..., of each segment the 16 rows blockIdx.y.  A
+// piece is acc [ROWS][D], m [ROWS], l [ROWS].  The warps take the rows, and share a row's pieces
+// where there are fewer rows.
+constexpr int kCombineWarps = 8, kCombineThreads = 32 * kCombineWarps;
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kCombineThreads) cache_combine_kernel(const CacheAttnArgs A)
+__global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const CacheAttnArgs A, int workers)
 {
     constexpr int kPart = ROWS * (D + 2), kPer = D / 32;
     __shared__ float sums[kCombineWarps][D];
     cudaGridDependencySynchronize();  // launched early: the pieces are there from here on
-    const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int4 meta = A.meta[w];
-    if (meta.z <= w) return;
-    int ts, n, len;
-    if (!load_span(A, meta.x, ts, n, len)) return;
-    const int tiles = (n * A.G + ROWS - 1) / ROWS;
-    const int head = meta.y / tiles, row0 = (meta.y - head * tiles) * ROWS + 16 * int(blockIdx.y);
-    const int rows = min(ROWS < 16 ? ROWS : 16, n * A.G - row0), pieces = meta.z - w + 1;
-    if (rows <= 0) return;
-    int groups = 1;
-    while (groups < rows) groups *= 2;
-    const int subs = kCombineWarps / groups, sub = warp / groups, r = warp % groups, rp = r + 16 * int(blockIdx.y);
-    auto part_of = [&](int p) { return A.part + int64_t(p == 0 ? meta.w : 2 * (w + p)) * kPart; };
-    float big = -INFINITY, total = 0.0f, out[kPer];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 mine = blockIdx.x + lane * gridDim.x < workers ? A.meta[2 * (blockIdx.x + lane * gridDim.x)] : make_int4(0, 0, 0, 0);
+    uint32_t found = __ballot_sync(0xffffffffu, mine.x > 0);
+    while (found) {
+        const int k = __ffs(found) - 1, w = blockIdx.x + k * gridDim.x;
+        found &= found - 1;
+        const int pieces = __shfl_sync(0xffffffffu, mine.x, k), slot0 = __shfl_sync(0xffffffffu, mine.y, k);
+        const int4 where = A.meta[2 * w + 1];  // first token, head, row of the segment in its head, its rows
+        const int row0 = where.z + 16 * int(blockIdx.y), rows = min(16, where.w - 16 * int(blockIdx.y));
+        if (rows <= 0) continue;
+        int groups = 1;
+        while (groups < rows && groups < kCombineWarps) groups *= 2;
+        const int subs = kCombineWarps / groups, sub = warp / groups;
+        for (int r = warp % groups; r < (subs > 1 ? groups : rows); r += groups) {
+            const int rp = r + 16 * int(blockIdx.y);
+            auto part_of = [&](int p) { return A.part + int64_t(p == 0 ? slot0 : 2 * (w + p)) * kPart; };
+            // A lane adds up kPer neighbouring channels of a row, kBatch pieces in flight at a time; the
+            // first batch is on its way while the weights are found.
+            constexpr int kBatch = 8;
+            float v[kBatch][kPer], vm[kBatch], big = -INFINITY, total = 0.0f, out[kPer];
+            auto load = [&](int p0) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) out[k] = 0.0f;
-    if (r < rows) {
-        for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + rp]);
+                for (int q = 0; q < kBatch; ++q) {
+                    const int p = p0 + q * subs;
+                    vm[q] = -INFINITY;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        const float ref = big == -INFINITY ? 0.0f : big;
-        for (int p = lane; p < pieces; p += 32) {
-            const float *part = part_of(p);
-            total += ex2_approx(part[ROWS * D + rp] - ref) * part[ROWS * (D + 1) + rp];
-        }
+                    for (int e = 0; e < kPer; ++e) v[q][e] = 0.0f;
+                    if (p < pieces && r < rows) {
+                        const float *part = part_of(p);
+                        vm[q] = part[ROWS * D + rp];
+                        load_floats(part + rp * D + lane * kPer, v[q]);
+                    }
+                }
+            };
+            load(sub);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-#pragma unroll 8
-        for (int p = sub; p < pieces; p += subs) {
-            const float *part = part_of(p);
-            const float f = ex2_approx(part[ROWS * D + rp] - ref);
+            for (int e = 0; e < kPer; ++e) out[e] = 0.0f;
+            if (r < rows) {
+                for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + rp]);
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) out[k] += f * part[rp * D + lane + 32 * k];
+                for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+            }
+            const float ref = big == -INFINITY ? 0.0f : big;
+            if (r < rows) {
+                for (int p = lane; p < pieces; p += 32) {
+                    const float *part = part_of(p);
+                    total += ex2_approx(part[ROWS * D + rp] - ref) * part[ROWS * (D + 1) + rp];
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            }
+            for (int p0 = sub;;) {
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    const float f = ex2_approx(vm[q] - ref);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) out[e] = fmaf(f, v[q][e], out[e]);
+                }
+                p0 += kBatch * subs;
+                if (p0 >= pieces) break;
+                load(p0);
+            }
+            if (subs > 1) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) sums[warp][lane * kPer + e] = out[e];
+                __syncthreads();
+                if (sub == 0)
+                    for (int y = 1; y < subs; ++y)
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) out[e] += sums[warp + y * groups][lane * kPer + e];
+                __syncthreads();
+            }
+            if (r >= rows || sub > 0) continue;
+            const float f = total == 0.0f ? 0.0f : 1.0f / total;
+            const int rr = row0 + r, i = rr / A.G;
+            const int64_t at = (int64_t(where.x) + i) * (A.H * A.G) + where.y * A.G + rr - i * A.G;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(A.o) + at * D + lane * kPer);
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_out(out[e] * f, out[e + 1] * f, T());
+            if (A.lse && lane == 0) A.lse[at] = total == 0.0f ? -INFINITY : (big + log2f(total)) * kLn2;
         }
     }
-    if (subs > 1) {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) sums[warp][lane + 32 * k] = out[k];
-        __syncthreads();
-        if (sub > 0) return;
-        for (int y = 1; y < subs; ++y)
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) out[k] += sums[warp + y * groups][lane + 32 * k];
-    }
-    if (r >= rows) return;
-    const float f = total == 0.0f ? 0.0f : 1.0f / total;
-    const int rr = row0 + r, i = rr / A.G;
-    const int64_t at = (int64_t(ts) + i) * (A.H * A.G) + head * A.G + rr - i * A.G;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        static_cast<uint16_t *>(A.o)[at * D + lane + 32 * k] = uint16_t(pack_out(out[k] * f, 0.0f, T()));
-    if (A.lse && lane == 0) A.lse[at] = total == 0.0f ? -INFINITY : (big + log2f(total)) * kLn2;
 }
 
 // The combine kernel is launched while the kernel before it still runs (it waits for its end on
-// the device), which hides its launch.
+// the device), which hides its launch.  One wave of blocks looks after all workers: as a block
+// for each worker, most of which have nothing to join, it took 14 us after 1776 workers.
 template <typename T, int D, int ROWS>
-cudaError_t launch_combine(const CacheAttnArgs &a, int workers, cudaStream_t st)
+cudaError_t launch_combine(const CacheAttnArgs &a, int workers, int sms, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(workers), ROWS <= 16 ? 1 : ROWS / 16);
+    cfg.gridDim = dim3(unsigned(std::min(workers, 6 * sms)), unsigned(cdiv(ROWS, 16)));
     cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -610,7 +657,7 @@ cudaError_t launch_combine(const CacheAttnArgs &a, int workers, cudaStream_t st)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_combine_kernel<T, D, ROWS>, a);
+    return cudaLaunchKernelEx(&cfg, cache_combine_kernel<T, D, ROWS>, a, workers);
 }
 
 template <typename T, int D, int NT>
@@ -622,7 +669,7 @@ cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const C
     if (e != cudaSuccess) return e;
     cache_attn_kernel<T, D, NT><<<sms, S::kThreads, S::kAlloc, st>>>(tm_k, tm_v, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_combine<T, D, S::kRows>(a, sms * S::kWarps, st);
+    return launch_combine<T, D, S::kRows>(a, sms * S::kWarps, sms, st);
 }
 
 template <typename T, int D>
@@ -630,14 +677,14 @@ cudaError_t launch_any(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const C
 {
     if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) {
         const cudaError_t e = launch_cache_chunk(a, sms, st);
-        return e == cudaSuccess ? launch_combine<T, D, 256>(a, sms, st) : e;
+        return e == cudaSuccess ? launch_combine<T, D, 256>(a, sms, sms, st) : e;
     }
     // two tiles of eight rows at once where most segments have more than eight
     if (int64_t(a.T) * a.G > int64_t(8) * a.B) return launch_for<T, D, 2>(tm_k, tm_v, a, sms, st);
     return launch_for<T, D, 1>(tm_k, tm_v, a, sms, st);
 }
 
-size_t meta_bytes(int sms) { return (size_t(sms) * kMaxWarps * sizeof(int4) + 255) & ~size_t(255); }
+size_t meta_bytes(int sms) { return (size_t(sms) * kMaxWarps * 2 * sizeof(int4) + 255) & ~size_t(255); }
 
 template <int D>
 size_t part_bytes(int sms)

@@ -812,8 +812,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 float *part = A.part + int64_t(slot) * S::kPart;
                 if (w.begins && !w.ends) {
                     split = true;
-                    if (t == 0 && wq == 0 && lane == 0)
-                        A.meta[wk] = make_int4(w.b, w.h * w.s.pairs + w.p, int((w.pos + w.r.steps() - 1) / chunk), slot);
+                    if (t == 0 && wq == 0 && lane == 0) {
+                        A.meta[2 * wk] = make_int4(int((w.pos + w.r.steps() - 1) / chunk) - wk + 1, slot, 0, 0);
+                        A.meta[2 * wk + 1] = make_int4(w.s.ts, w.h, w.p * kRowsSeg, min(kRowsSeg, w.s.n * A.G - w.p * kRowsSeg));
+                    }
                 }
                 if (valid && whole && A.lse) A.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
                 if (valid && !whole) {
@@ -849,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
             ++o;
         }
         // tile A takes part in every piece, so it knows whether a segment was begun and not ended
-        if (warp == 0 && lane == 0 && !split) A.meta[wk] = make_int4(0, 0, 0, 0);
+        if (warp == 0 && lane == 0 && !split) A.meta[2 * wk] = make_int4(0, 0, 0, 0);
     }
     if (lane == 0 && !ok) {
         *abort_flag = 1;
