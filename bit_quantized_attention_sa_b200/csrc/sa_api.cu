@@ -441,7 +441,7 @@ static sa_status check_cache(int64_t T, int B, int H, int d, int max_pages, int 
     if (d != 64 && d != 128) return SA_ERR_UNSUPPORTED;
     // lines of 128 bytes are a 32-bit TMA coordinate; positions and grid dimensions likewise
     if (T > (1 << 30) || B > (1 << 20) || H > 65535 || max_pages > (1 << 30) / kPage ||
-        int64_t(num_pages) * H > (int64_t(INT_MAX) * 2) / d)
+        int64_t(num_pages) * H > (int64_t(INT_MAX) * 2) / d || (T / kPage + 2 * int64_t(B)) * H > INT_MAX)
         return SA_ERR_UNSUPPORTED;
     if (T == 0) return SA_OK;
     for (const void *p : {tok_start, kv_lens, table, k_codes, k_scale, v_codes, v_scale})

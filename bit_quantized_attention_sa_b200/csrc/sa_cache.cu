@@ -12,9 +12,11 @@
 // reads back as NaN instead of hiding it.
 //
 // What bounds it: two bytes read and one written per value; for one token a sequence, the
-// chain of dependent loads (sequence, length, page, scale).  One block of threads takes one
-// (block of tokens, head): half of it the keys, half the values, which stay in registers
-// between the maximum and the codes.
+// chain of dependent loads (sequence, page, scale).  One block of threads takes one block of
+// tokens and some heads, half of it the keys, half the values; a head's values stay in
+// registers between the maximum and the codes.
+#include <algorithm>
+#include <climits>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,8 +29,8 @@ __device__ int g_cache_status;  // 0 = OK, 8 = an index read on the device was o
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kHalf = kThreads / 2;
+constexpr int kVec = 4;    // 8-value chunks of a thread
+constexpr int kWaves = 6;  // blocks of threads an SM, at least, before a block takes more heads
 
 __device__ __forceinline__ void record_bad_index() { atomicExch(&g_cache_status, 8); }
 
@@ -41,21 +43,38 @@ struct Place {
     bool first;  // the sequence's first slot
 };
 
+template <int kThreads>
 __device__ __forceinline__ bool find_place(const CacheArgs &A, int slot, Place &P)
 {
-    // base is increasing in b: b is the number of bases at or below the slot, less one
+    // base is increasing in b: b is the last one whose base is at or below the slot; the thread
+    // that looks at it has the rest of what there is to know already on its way
+    __shared__ int found[4];
     int below = 0;
     for (int i = 0; i < A.B; i += kThreads) {
         const int b = i + int(threadIdx.x);
-        const int c = __syncthreads_count(b < A.B && A.tok_start[b] / kPage + 2 * b <= slot);
+        int ts = 0, te = 0, len = 0;
+        if (b < A.B) {
+            ts = A.tok_start[b];
+            te = A.tok_start[b + 1];
+            len = A.kv_lens[b];
+        }
+        const bool in = b < A.B && ts / kPage + 2 * b <= slot;
+        const int c = __syncthreads_count(in);
+        if (in && int(threadIdx.x) == c - 1) {
+            found[0] = b;
+            found[1] = ts;
+            found[2] = te;
+            found[3] = len;
+        }
         below += c;
         if (c < kThreads) break;
     }
-    P.b = below - 1;
-    if (P.b < 0) return false;
-    P.ts = A.tok_start[P.b];
-    const int te = A.tok_start[P.b + 1];
-    P.len = A.kv_lens[P.b];
+    __syncthreads();
+    if (below == 0) return false;
+    P.b = found[0];
+    P.ts = found[1];
+    const int te = found[2];
+    P.len = found[3];
     P.n = te - P.ts;
     if (P.ts < 0 || te < P.ts || te > A.T || P.len < 0 || P.len > int64_t(A.max_pages) * kPage) {
         if (threadIdx.x == 0) record_bad_index();
@@ -99,92 +118,119 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
 
 __device__ __forceinline__ int clamp127(float q) { return max(-127, min(127, __float2int_rn(q))); }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheArgs A)
+// Four codes rint(fl(x / s)) from the reciprocal r of s, correctly rounded: one step of Newton's
+// iteration with the exact remainder, q = x r, q + (x - q s) r, gives the correctly rounded
+// quotient (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) as long as nothing leaves the normal range, which the caller sees to.  Adding
+// 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the low bits.
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float s, float r)
 {
-    constexpr int kChunks = D / 8;             // 8-value chunks of a row
-    constexpr int kVec = kPage * kChunks / kHalf;  // chunks of a thread
-    __shared__ uint32_t most[kThreads / 32];
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float q = x[i] * r;
+        y[i] = __float_as_uint(fmaf(fmaf(-q, s, x[i]), r, q) + 12582912.0f);
+    }
+    return __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) cache_append_kernel(const CacheArgs A)
+{
+    constexpr int kThreads = 4 * D, kHalf = kThreads / 2;
+    constexpr int kChunks = D / 8;  // 8-value chunks of a row
+    static_assert(kVec * kHalf == kPage * kChunks, "a block's chunks");
+    __shared__ uint32_t most[2][kThreads / 32];
     Place P;
-    if (!find_place(A, blockIdx.x, P) || P.page < 0) return;
-    const int head = blockIdx.y, side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
-    const T *src = static_cast<const T *>(side ? A.v : A.k);
-    const int64_t stride = side ? A.v_stride : A.k_stride;
-    const int64_t cell = int64_t(P.page) * A.H + head;
-    int8_t *codes = (side ? A.v_codes : A.k_codes) + cell * (kPage * D);
-    float *scale = (side ? A.v_scale : A.k_scale) + cell;
+    if (!find_place<kThreads>(A, int(blockIdx.x) / A.head_cuts, P) || P.page < 0) return;
+    const int side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
+    const int h_lo = int(blockIdx.x) % A.head_cuts * A.heads_per_block, h_hi = min(A.H, h_lo + A.heads_per_block);
     const int row_lo = P.lo - P.block * kPage, row_hi = P.hi - P.block * kPage;  // new rows
-    const float s_old = row_lo > 0 ? *scale : 0.0f;
+    const int64_t stride = side ? A.v_stride : A.k_stride;
+    const T *src = static_cast<const T *>(side ? A.v : A.k) + (P.ts + int64_t(P.block * kPage - P.start)) * stride;
+    int8_t *codes = (side ? A.v_codes : A.k_codes) + int64_t(P.page) * A.H * (kPage * D);
+    float *scale = (side ? A.v_scale : A.k_scale) + int64_t(P.page) * A.H;
 
-    uint4 x[kVec];
-    uint32_t top = 0;  // two 16-bit maxima of |x|'s bits
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int v = tid + i * kHalf, row = v / kChunks, c = v % kChunks;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (row >= row_lo && row < row_hi) {
-            const int64_t t = P.ts + (P.block * kPage + row - P.start);
-            x[i] = *reinterpret_cast<const uint4 *>(src + t * stride + head * D + 8 * c);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-    }
-    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x / 32] = top;
-    __syncthreads();
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kHalf / 32; ++i) m = max(m, most[side * (kHalf / 32) + i]);
-    const float s_new = __fdiv_rn(bits_to_float<T>(m), 127.0f);
-    const float s = (row_lo == 0 || s_new > s_old || s_new != s_new) ? s_new : s_old;
-
-    if (row_lo > 0 && !(s == s_old)) {
-        const float r = __fdiv_rn(s_old, s);
+    for (int head = h_lo; head < h_hi; ++head) {
+        uint4 x[kVec];
+        uint32_t top = 0;  // two 16-bit maxima of |x|'s bits
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const int v = tid + i * kHalf;
-            if (v / kChunks >= row_lo) continue;
-            uint2 *p = reinterpret_cast<uint2 *>(codes + 8 * v);
-            const uint2 w = *p;
-            int c[8];
+            const int v = tid + i * kHalf, row = v / kChunks, c = v % kChunks;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (row >= row_lo && row < row_hi)
+                x[i] = *reinterpret_cast<const uint4 *>(src + row * stride + head * D + 8 * c);
+        }
+        const float s_old = row_lo > 0 ? scale[head] : 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int code = int(int8_t((k < 4 ? w.x : w.y) >> (8 * (k & 3))));
-                c[k] = clamp127(__fmul_rn(float(code), r));
+        for (int i = 0; i < kVec; ++i)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                         __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        uint32_t *turn = most[head & 1];
+        if ((threadIdx.x & 31) == 0) turn[threadIdx.x / 32] = top;
+        __syncthreads();
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kHalf / 32; ++i) m = max(m, turn[side * (kHalf / 32) + i]);
+        const float s_new = __fdiv_rn(bits_to_float<T>(m), 127.0f);
+        const float s = (row_lo == 0 || s_new > s_old || s_new != s_new) ? s_new : s_old;
+        int8_t *cell = codes + int64_t(head) * (kPage * D);
+
+        if (row_lo > 0 && !(s == s_old)) {
+            const float r = __fdiv_rn(s_old, s);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int v = tid + i * kHalf;
+                if (v / kChunks >= row_lo) continue;
+                uint2 *p = reinterpret_cast<uint2 *>(cell + 8 * v);
+                const uint2 w = *p;
+                int c[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int code = int(int8_t((k < 4 ? w.x : w.y) >> (8 * (k & 3))));
+                    c[k] = clamp127(__fmul_rn(float(code), r));
+                }
+                *p = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
             }
-            *p = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
         }
-    }
+        const float r = __frcp_rn(s);
+        const bool plain = s >= 7.9e-31f && s <= 1.26e30f;  // 2^-100, 2^100: x and quotients stay normal, or round to 0
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int v = tid + i * kHalf, row = v / kChunks;
-        if (row < row_lo || row >= row_hi) continue;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        int c[8];
+        for (int i = 0; i < kVec; ++i) {
+            const int v = tid + i * kHalf, row = v / kChunks;
+            if (row < row_lo || row >= row_hi) continue;
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t out[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float f = bits_to_float<T>((w[k / 2] >> (16 * (k & 1))) & 0xffffu);
-            c[k] = s == 0.0f ? 0 : clamp127(__fdiv_rn(f, s));
+            for (int y = 0; y < 2; ++y) {
+                const float f[4] = {bits_to_float<T>(w[2 * y] & 0xffffu), bits_to_float<T>(w[2 * y] >> 16),
+                                    bits_to_float<T>(w[2 * y + 1] & 0xffffu), bits_to_float<T>(w[2 * y + 1] >> 16)};
+                if (plain) {
+                    out[y] = codes4(f, s, r);
+                } else {
+                    int c[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) c[k] = s == 0.0f ? 0 : clamp127(__fdiv_rn(f[k], s));
+                    out[y] = pack4(c[0], c[1], c[2], c[3]);
+                }
+            }
+            *reinterpret_cast<uint2 *>(cell + 8 * v) = make_uint2(out[0], out[1]);
         }
-        *reinterpret_cast<uint2 *>(codes + 8 * v) =
-            make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+        if (tid == 0) scale[head] = s;
     }
-    if (tid == 0) *scale = s;
 }
 
+// 16 bytes of output
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&f)[8]);
+__device__ __forceinline__ void store16(T *p, const float (&f)[16 / sizeof(T)]);
 template <>
-__device__ __forceinline__ void store8<float>(float *p, const float (&f)[8])
+__device__ __forceinline__ void store16<float>(float *p, const float (&f)[4])
 {
     *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
 }
 template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *p, const float (&f)[8])
+__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16 *p, const float (&f)[8])
 {
     uint32_t w[4];
 #pragma unroll
@@ -195,7 +241,7 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *p, const fl
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <>
-__device__ __forceinline__ void store8<__half>(__half *p, const float (&f)[8])
+__device__ __forceinline__ void store16<__half>(__half *p, const float (&f)[8])
 {
     uint32_t w[4];
 #pragma unroll
@@ -206,74 +252,97 @@ __device__ __forceinline__ void store8<__half>(__half *p, const float (&f)[8])
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs A)
+// N codes from p on as floats
+template <int N>
+__device__ __forceinline__ void load_codes(const int8_t *p, float (&f)[N])
 {
-    constexpr int kChunks = D / 8;
-    constexpr int kVec = kPage * kChunks / kHalf;
+    if constexpr (N == 8) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = float(int8_t((k < 4 ? w.x : w.y) >> (8 * (k & 3))));
+    } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = float(int8_t(w >> (8 * k)));
+    }
+}
+
+// Writes are most of it, so a thread takes as many codes as fill 16 bytes of the output.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheArgs A)
+{
+    constexpr int kThreads = 256, kHalf = kThreads / 2, kCodes = 16 / int(sizeof(T)), kChunks = D / kCodes;
+    constexpr int kPer = kPage * kChunks / kHalf;
     Place P;
-    if (!find_place(A, blockIdx.x, P)) return;
-    const int head = blockIdx.y, side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
+    if (!find_place<kThreads>(A, int(blockIdx.x) / A.H, P)) return;
+    const int head = int(blockIdx.x) % A.H, side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
     T *dst = static_cast<T *>(const_cast<void *>(side ? A.v : A.k));
     if (!dst) return;
     const int64_t stride = int64_t(A.H) * D;
     if (P.first && P.start < 0) {  // positions before the sequence: zero
-        const float zero[8] = {};
-        for (int i = tid; i < min(-P.start, P.n) * kChunks; i += kHalf)
-            store8<T>(dst + (P.ts + int64_t(i / kChunks)) * stride + head * D + 8 * (i % kChunks), zero);
+        const float zero[kCodes] = {};
+        for (int64_t i = tid; i < int64_t(min(-P.start, P.n)) * kChunks; i += kHalf)
+            store16<T>(dst + (P.ts + i / kChunks) * stride + head * D + kCodes * (i % kChunks), zero);
     }
     if (P.lo >= P.hi) return;
     const int64_t cell = int64_t(max(P.page, 0)) * A.H + head;
     const int8_t *codes = (side ? A.v_codes : A.k_codes) + cell * (kPage * D);
     const float s = P.page < 0 ? __int_as_float(0x7fffffff) : (side ? A.v_scale : A.k_scale)[cell];
     const int row_lo = P.lo - P.block * kPage, row_hi = P.hi - P.block * kPage;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    dst += (P.ts + int64_t(P.block * kPage - P.start)) * stride + head * D;
+#pragma unroll 8
+    for (int i = 0; i < kPer; ++i) {
         const int v = tid + i * kHalf, row = v / kChunks, c = v % kChunks;
         if (row < row_lo || row >= row_hi) continue;
-        const uint2 w = *reinterpret_cast<const uint2 *>(codes + 8 * v);
-        float f[8];
+        float f[kCodes];
+        load_codes(codes + kCodes * v, f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = float(int8_t((k < 4 ? w.x : w.y) >> (8 * (k & 3)))) * s;
-        const int64_t t = P.ts + (P.block * kPage + row - P.start);
-        store8<T>(dst + t * stride + head * D + 8 * c, f);
+        for (int k = 0; k < kCodes; ++k) f[k] *= s;
+        store16<T>(dst + row * stride + kCodes * c, f);
     }
 }
 
-template <typename T>
-cudaError_t append_for(const CacheArgs &a, dim3 grid, cudaStream_t st)
+// Neighbouring blocks take the heads of the same tokens, whose memory is contiguous.
+int64_t slots_of(const CacheArgs &a) { return a.T / kPage + 2 * int64_t(a.B); }
+
+template <typename T, int D>
+cudaError_t append_for(CacheArgs a, cudaStream_t st)
 {
-    if (a.d == 128)
-        cache_append_kernel<T, 128><<<grid, kThreads, 0, st>>>(a);
-    else
-        cache_append_kernel<T, 64><<<grid, kThreads, 0, st>>>(a);
+    // several heads a block where there are blocks enough to fill the SMs several times over
+    const int64_t blocks = (a.T / kPage + a.B) * int64_t(a.H);  // about so many are not empty
+    a.heads_per_block = int(std::max<int64_t>(1, std::min<int64_t>(8, blocks / (kWaves * std::max(1, device_sms())))));
+    a.head_cuts = int(cdiv(a.H, a.heads_per_block));
+    const int64_t grid = slots_of(a) * a.head_cuts;
+    if (grid > INT_MAX) return cudaErrorInvalidValue;
+    cache_append_kernel<T, D><<<unsigned(grid), 4 * D, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t read_for(const CacheArgs &a, dim3 grid, cudaStream_t st)
+cudaError_t read_for(const CacheArgs &a, cudaStream_t st)
 {
+    const int64_t grid = slots_of(a) * a.H;
+    if (grid > INT_MAX) return cudaErrorInvalidValue;
     if (a.d == 128)
-        cache_read_kernel<T, 128><<<grid, kThreads, 0, st>>>(a);
+        cache_read_kernel<T, 128><<<unsigned(grid), 256, 0, st>>>(a);
     else
-        cache_read_kernel<T, 64><<<grid, kThreads, 0, st>>>(a);
+        cache_read_kernel<T, 64><<<unsigned(grid), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
-
-dim3 place_grid(const CacheArgs &a) { return dim3(unsigned(a.T / kPage + 2 * a.B), unsigned(a.H)); }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheArgs &a, int dtype, cudaStream_t st)
 {
-    return dtype == 0 ? append_for<__nv_bfloat16>(a, place_grid(a), st) : append_for<__half>(a, place_grid(a), st);
+    if (dtype == 0) return a.d == 128 ? append_for<__nv_bfloat16, 128>(a, st) : append_for<__nv_bfloat16, 64>(a, st);
+    return a.d == 128 ? append_for<__half, 128>(a, st) : append_for<__half, 64>(a, st);
 }
 
 cudaError_t launch_cache_read(const CacheArgs &a, int dtype, cudaStream_t st)
 {
-    if (dtype == 0) return read_for<__nv_bfloat16>(a, place_grid(a), st);
-    if (dtype == 1) return read_for<__half>(a, place_grid(a), st);
-    return read_for<float>(a, place_grid(a), st);
+    if (dtype == 0) return read_for<__nv_bfloat16>(a, st);
+    if (dtype == 1) return read_for<__half>(a, st);
+    return read_for<float>(a, st);
 }
 
 cudaError_t read_and_clear_cache_status(int *status)

@@ -138,6 +138,7 @@ struct CacheArgs {
     float *k_scale = nullptr, *v_scale = nullptr;
     const int32_t *tok_start = nullptr, *kv_lens = nullptr, *table = nullptr;
     int T = 0, B = 0, H = 0, d = 0, max_pages = 0, num_pages = 0;
+    int heads_per_block = 1, head_cuts = 1;  // set by the launcher
 };
 cudaError_t launch_cache_append(const CacheArgs &a, int dtype, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheArgs &a, int dtype, cudaStream_t st);

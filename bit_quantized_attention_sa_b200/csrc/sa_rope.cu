@@ -97,7 +97,7 @@ struct Vec8<__half> : Vec8Half<__half, __half2> {
     }
 };
 
-template <typename T>
+template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A)
 {
     __shared__ float2 table[kTileUnits * 8];  // [token of the tile][pair]
@@ -107,10 +107,46 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A)
     const int n0 = int(blockIdx.x % tiles) * tile_tokens;
     const int ntok = min(tile_tokens, A.N - n0);
 
+    const int tu = tile_tokens * units, slots = kThreads / tu;
+    const int slot = threadIdx.x / tu, rest = threadIdx.x - slot * tu;
+    const int t = rest / units, u = rest - t * units;
+    const bool active = slot < slots && t < ntok;
+    // The thread's two chunks of 8 channels, each contiguous from thread to thread: the two halves of
+    // eight pairs, or (interleaved, and channels that do not turn) four pairs each.
+    const bool pairs = !INTERLEAVED && 16 * u < A.rot;
+    const int c0 = INTERLEAVED || pairs ? 8 * u : 8 * u + half;
+    const int c1 = INTERLEAVED ? A.d / 2 + 8 * u : pairs ? half + 8 * u : c0 + (A.d - A.rot) / 2;
+    const bool turned0 = INTERLEAVED ? c0 < A.rot : pairs, turned1 = INTERLEAVED ? c1 < A.rot : pairs;
+    const int heads = A.io[0].heads + A.io[1].heads;
+    const int h_end = min(heads, int(blockIdx.y + 1) * A.heads_per_block);
+    int h0 = blockIdx.y * A.heads_per_block + slot;
+
+    constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
+    Vec8<T> lo[kUnroll], hi[kUnroll];
+    T *dst[kUnroll];
+    auto load = [&]() {
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const int h = h0 + k * slots;
+            dst[k] = nullptr;
+            if (!active || h >= h_end) continue;
+            const bool second = h >= A.io[0].heads;
+            const RopeIo &io = A.io[second ? 1 : 0];
+            const int64_t hh = second ? h - A.io[0].heads : h, n = n0 + t;
+            const T *src = static_cast<const T *>(io.x) + b * io.xb + hh * io.xh + n * io.xn;
+            T *out = static_cast<T *>(io.y) + b * io.yb + hh * io.yh + n * io.yn;
+            if (!turned0 && !turned1 && src == out) continue;  // in place: nothing to copy
+            dst[k] = out;
+            lo[k].load(src + c0);
+            hi[k].load(src + c1);
+        }
+    };
+    load();  // on their way while the sines are found
+
     for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
+        const int ti = i / half, p = i - ti * half;
         const int axis = (p >= A.axis_end[0]) + (p >= A.axis_end[1]) + (p >= A.axis_end[2]);
-        const int pos = A.pos[axis * A.pos_axis_stride + b * A.pos_batch_stride + n0 + t];
+        const int pos = A.pos[axis * A.pos_axis_stride + b * A.pos_batch_stride + n0 + ti];
         // whole turns drop out: 0.15915... = 1 / (2 pi)
         const double turns = double(pos) * (A.freqs[p] * 0.15915494309189533577);
         float s, c;
@@ -118,72 +154,37 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A)
         table[i] = make_float2(c * A.amplitude, s * (A.inverse ? -A.amplitude : A.amplitude));
     }
     __syncthreads();
-
-    const int tu = tile_tokens * units, slots = kThreads / tu;
-    const int slot = threadIdx.x / tu, rest = threadIdx.x - slot * tu;
-    const int t = rest / units, u = rest - t * units;
-    if (slot >= slots || t >= ntok) return;
-    const bool turned = 16 * u < A.rot;
-    const int c0 = turned && !A.interleaved ? 8 * u : 16 * u;
-    const int c1 = turned && !A.interleaved ? half + 8 * u : 16 * u + 8;
+    if (!active) return;
     float cs[8], sn[8];
-    if (turned) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 w = table[t * half + 8 * u + i];
-            cs[i] = w.x;
-            sn[i] = w.y;
-        }
+    for (int i = 0; i < 8; ++i) {
+        const int p = INTERLEAVED ? ((i < 4 ? c0 : c1) / 2 + (i & 3)) : c0 + i;
+        const float2 w = (i < 4 ? turned0 : turned1) ? table[t * half + p] : make_float2(1.0f, 0.0f);
+        cs[i] = w.x;
+        sn[i] = w.y;
     }
-    const int heads = A.io[0].heads + A.io[1].heads;
-    const int h_end = min(heads, int(blockIdx.y + 1) * A.heads_per_block);
-    constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
-    for (int h0 = blockIdx.y * A.heads_per_block + slot; h0 < h_end; h0 += kUnroll * slots) {
-        Vec8<T> lo[kUnroll], hi[kUnroll];
-        T *dst[kUnroll];
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int h = h0 + k * slots;
-            dst[k] = nullptr;
-            if (h >= h_end) continue;
-            const bool second = h >= A.io[0].heads;
-            const RopeIo &io = A.io[second ? 1 : 0];
-            const int64_t hh = second ? h - A.io[0].heads : h, n = n0 + t;
-            const T *src = static_cast<const T *>(io.x) + b * io.xb + hh * io.xh + n * io.xn;
-            T *out = static_cast<T *>(io.y) + b * io.yb + hh * io.yh + n * io.yn;
-            if (!turned && src == out) continue;  // in place: nothing to copy
-            dst[k] = out;
-            lo[k].load(src + c0);
-            hi[k].load(src + c1);
-        }
+    while (true) {
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
             if (!dst[k]) continue;
             float x[8], y[8];
             lo[k].get(x);
             hi[k].get(y);
-            if (turned) {
-                if (A.interleaved) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = x[2 * i], e = x[2 * i + 1], f = y[2 * i], g = y[2 * i + 1];
-                        x[2 * i] = a * cs[i] - e * sn[i];
-                        x[2 * i + 1] = e * cs[i] + a * sn[i];
-                        y[2 * i] = f * cs[4 + i] - g * sn[4 + i];
-                        y[2 * i + 1] = g * cs[4 + i] + f * sn[4 + i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = x[i], e = y[i];
-                        x[i] = a * cs[i] - e * sn[i];
-                        y[i] = e * cs[i] + a * sn[i];
-                    }
-                }
+            for (int i = 0; i < 8; ++i) {
+                if (!(i < 4 ? turned0 : turned1)) continue;
+                float &p = INTERLEAVED ? (i < 4 ? x[2 * i & 7] : y[2 * i & 7]) : x[i];
+                float &q = INTERLEAVED ? (i < 4 ? x[(2 * i + 1) & 7] : y[(2 * i + 1) & 7]) : y[i];
+                const float a = p, e = q;
+                p = a * cs[i] - e * sn[i];
+                q = e * cs[i] + a * sn[i];
             }
             Vec8<T>::store(dst[k] + c0, x);
             Vec8<T>::store(dst[k] + c1, y);
         }
+        h0 += kUnroll * slots;
+        if (h0 >= h_end) break;
+        load();
     }
 }
 
@@ -203,11 +204,14 @@ cudaError_t launch_rope(RopeArgs a, int dtype, cudaStream_t st)
     a.heads_per_block = int(cdiv(heads, cuts));
     const dim3 grid(unsigned(tiles), unsigned(cdiv(heads, a.heads_per_block)));
     if (dtype == 0)
-        rope_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
+        a.interleaved ? rope_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, st>>>(a)
+                      : rope_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, st>>>(a);
     else if (dtype == 1)
-        rope_kernel<__half><<<grid, kThreads, 0, st>>>(a);
+        a.interleaved ? rope_kernel<__half, true><<<grid, kThreads, 0, st>>>(a)
+                      : rope_kernel<__half, false><<<grid, kThreads, 0, st>>>(a);
     else
-        rope_kernel<float><<<grid, kThreads, 0, st>>>(a);
+        a.interleaved ? rope_kernel<float, true><<<grid, kThreads, 0, st>>>(a)
+                      : rope_kernel<float, false><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

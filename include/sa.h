@@ -302,7 +302,8 @@ sa_status sa_sla_fwd(const void *q, const void *k, const void *v, void *o, int B
  *   - The codes, k, v, q, o, x, y and the workspace are 16-byte aligned; freqs 8-byte; the int32
  *     and the other fp32 arrays 4-byte.  Token strides are in elements, multiples of 16 bytes, and at
  *     least a token's heads * d; a token's heads follow each other without a gap.  B <= 2^20,
- *     T <= 2^30, H <= 65535, 64 * max_pages <= 2^30, num_pages * H * d / 2 <= 2^31 - 1.
+ *     T <= 2^30, H <= 65535, 64 * max_pages <= 2^30, num_pages * H * d / 2 <= 2^31 - 1 and
+ *     (T / 64 + 2 B) * H <= 2^31 - 1, else SA_ERR_UNSUPPORTED.
  *   - No call uses the library workspace or allocates anything. */
 enum { SA_BF16 = 0, SA_FP16 = 1, SA_FP32 = 2 };
 enum { SA_ROPE_PLAIN = 0, SA_ROPE_LINEAR = 1, SA_ROPE_BASE = 2, SA_ROPE_RAMP = 3 };
