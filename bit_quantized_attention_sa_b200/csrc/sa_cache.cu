@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) cache_append_kernel(con
     constexpr int kChunks = D / 8;  // 8-value chunks of a row
     static_assert(kVec * kHalf == kPage * kChunks, "a block's chunks");
     __shared__ uint32_t most[2][kThreads / 32];
+    chain_begin();
     Place P;
     if (!find_place<kThreads>(A, int(blockIdx.x) / A.head_cuts, P) || P.page < 0) return;
     const int side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheArgs A)
 {
     constexpr int kThreads = 256, kHalf = kThreads / 2, kCodes = 16 / int(sizeof(T)), kChunks = D / kCodes;
     constexpr int kPer = kPage * kChunks / kHalf;
+    chain_begin();
     Place P;
     if (!find_place<kThreads>(A, int(blockIdx.x) / A.H, P)) return;
     const int head = int(blockIdx.x) % A.H, side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
@@ -314,8 +316,7 @@ cudaError_t append_for(CacheArgs a, cudaStream_t st)
     a.head_cuts = int(cdiv(a.H, a.heads_per_block));
     const int64_t grid = slots_of(a) * a.head_cuts;
     if (grid > INT_MAX) return cudaErrorInvalidValue;
-    cache_append_kernel<T, D><<<unsigned(grid), 4 * D, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained(cache_append_kernel<T, D>, dim3(unsigned(grid)), 4 * D, 0, st, a);
 }
 
 template <typename T>
@@ -323,11 +324,7 @@ cudaError_t read_for(const CacheArgs &a, cudaStream_t st)
 {
     const int64_t grid = slots_of(a) * a.H;
     if (grid > INT_MAX) return cudaErrorInvalidValue;
-    if (a.d == 128)
-        cache_read_kernel<T, 128><<<unsigned(grid), 256, 0, st>>>(a);
-    else
-        cache_read_kernel<T, 64><<<unsigned(grid), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained(a.d == 128 ? cache_read_kernel<T, 128> : cache_read_kernel<T, 64>, dim3(unsigned(grid)), 256, 0, st, a);
 }
 
 }  // namespace

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
 
+    chain_begin();
     // ---- the flattened work: thread t sums the sequences [t * per, (t + 1) * per)
     const int per = (A.B + kThreads - 1) / kThreads;
     int64_t mine = 0;
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
 {
     constexpr int kPart = ROWS * (D + 2), kPer = D / 32;
     __shared__ float sums[kCombineWarps][D];
-    cudaGridDependencySynchronize();  // launched early: the pieces are there from here on
+    chain_begin();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 mine = blockIdx.x + lane * gridDim.x < workers ? A.meta[2 * (blockIdx.x + lane * gridDim.x)] : make_int4(0, 0, 0, 0);
     uint32_t found = __ballot_sync(0xffffffffu, mine.x > 0);
@@ -642,22 +643,13 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
     }
 }
 
-// The combine kernel is launched while the kernel before it still runs (it waits for its end on
-// the device), which hides its launch.  One wave of blocks looks after all workers: as a block
-// for each worker, most of which have nothing to join, it took 14 us after 1776 workers.
+// One wave of blocks looks after all workers: as a block for each worker, most of which have
+// nothing to join, it took 14 us after 1776 workers.
 template <typename T, int D, int ROWS>
 cudaError_t launch_combine(const CacheAttnArgs &a, int workers, int sms, cudaStream_t st)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min(workers, 6 * sms)), unsigned(cdiv(ROWS, 16)));
-    cfg.blockDim = dim3(kCombineThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_combine_kernel<T, D, ROWS>, a, workers);
+    return launch_chained(cache_combine_kernel<T, D, ROWS>, dim3(unsigned(std::min(workers, 6 * sms)), unsigned(cdiv(ROWS, 16))),
+                          kCombineThreads, 0, st, a, workers);
 }
 
 template <typename T, int D, int NT>
@@ -667,8 +659,8 @@ cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const C
     cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(S::kAlloc));
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<T, D, NT><<<sms, S::kThreads, S::kAlloc, st>>>(tm_k, tm_v, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_chained(cache_attn_kernel<T, D, NT>, dim3(unsigned(sms)), S::kThreads, S::kAlloc, st, tm_k, tm_v, a);
+    if (e != cudaSuccess) return e;
     return launch_combine<T, D, S::kRows>(a, sms * S::kWarps, sms, st);
 }
 

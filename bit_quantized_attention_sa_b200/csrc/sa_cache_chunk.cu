@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         fence_barrier_init();
     }
     if (warp == kWarpQK) tmem_alloc(smem_u32(tmem_word), kTmemCols);
+    chain_begin();
     // ---- the work: a warp sums a sequence's segments, or with many sequences each thread one's
     if (A.B > 64) {
         for (int b = threadIdx.x; b < A.B; b += kThreads) {
@@ -869,8 +870,7 @@ cudaError_t launch_for(const CacheAttnArgs &a, int sms, cudaStream_t st)
     cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(Sizes<D>::kAlloc));
     if (e != cudaSuccess) return e;
-    cache_chunk_kernel<T, D><<<sms, kThreads, Sizes<D>::kAlloc, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained(cache_chunk_kernel<T, D>, dim3(unsigned(sms)), kThreads, Sizes<D>::kAlloc, st, a);
 }
 
 }  // namespace

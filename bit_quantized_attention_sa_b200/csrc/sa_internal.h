@@ -109,6 +109,33 @@ cudaError_t launch_sla_linear(const void *q, const void *k, const void *v, const
 cudaError_t launch_sla_critical(const uint8_t *classes, int64_t n, uint8_t *keep, cudaStream_t st);
 cudaError_t read_and_clear_sla_status(int *status);
 int device_sms();  // of the current device (sa_api.cu)
+// Launches a kernel that begins with chain_begin(): it may be brought onto the SMs while the
+// kernel before it on the stream runs out, and waits there for its end.  Used by the serving
+// kernels, which follow one another at a few microseconds each.
+template <typename... P, typename... V>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, V &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+#ifdef __CUDACC__
+// First thing in such a kernel: lets the next one come, and waits until everything before is
+// done and visible.
+__device__ __forceinline__ void chain_begin()
+{
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+}
+#endif
 // ---- rotary positions (sa_rope.cu)
 struct RopeIo {
     const void *x = nullptr;

@@ -101,6 +101,7 @@ template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A)
 {
     __shared__ float2 table[kTileUnits * 8];  // [token of the tile][pair]
+    chain_begin();
     const int units = A.d / 16, tile_tokens = A.tile_tokens, half = A.rot / 2;
     const int tiles = (A.N + tile_tokens - 1) / tile_tokens;
     const int64_t b = blockIdx.x / tiles;
@@ -203,16 +204,10 @@ cudaError_t launch_rope(RopeArgs a, int dtype, cudaStream_t st)
     while (tiles * cuts < 2 * sms && cdiv(heads, cuts) > slots) ++cuts;
     a.heads_per_block = int(cdiv(heads, cuts));
     const dim3 grid(unsigned(tiles), unsigned(cdiv(heads, a.heads_per_block)));
-    if (dtype == 0)
-        a.interleaved ? rope_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, st>>>(a)
-                      : rope_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, st>>>(a);
-    else if (dtype == 1)
-        a.interleaved ? rope_kernel<__half, true><<<grid, kThreads, 0, st>>>(a)
-                      : rope_kernel<__half, false><<<grid, kThreads, 0, st>>>(a);
-    else
-        a.interleaved ? rope_kernel<float, true><<<grid, kThreads, 0, st>>>(a)
-                      : rope_kernel<float, false><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    auto go = [&](void (*kernel)(RopeArgs)) { return launch_chained(kernel, grid, kThreads, 0, st, a); };
+    if (dtype == 0) return go(a.interleaved ? rope_kernel<__nv_bfloat16, true> : rope_kernel<__nv_bfloat16, false>);
+    if (dtype == 1) return go(a.interleaved ? rope_kernel<__half, true> : rope_kernel<__half, false>);
+    return go(a.interleaved ? rope_kernel<float, true> : rope_kernel<float, false>);
 }
 
 }  // namespace sa

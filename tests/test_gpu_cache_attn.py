@@ -199,12 +199,12 @@ def test_captured_steps_follow_lengths(libsa, cuda_ok):
         torch.cuda.current_stream().wait_stream(s)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
+            pos.copy_(lens).sub_(1).clamp_(min=0)    # other nodes before and between the library's
             outs.append(_step(libsa, cache[i], qkv, pos, starts, lens, table, freqs, H, G))
         graphs.append(g)
     for _ in range(70):
         qkv.copy_(torch.randn(qkv.shape, generator=gen))
         lens += torch.tensor([1, 1, 0, 1], dtype=torch.int32, device="cuda")
-        pos.copy_((lens - 1).clamp(min=0))
         graphs[0].replay()
         want = _step(libsa, cache[2], qkv, pos, starts, lens, table, freqs, H, G)
         graphs[1].replay()
