@@ -327,14 +327,6 @@ __device__ __forceinline__ void p32_any(const uint32_t (&s)[32], float c, float 
     }
 }
 
-// bits lo..hi-1 (clamped) of a 32-bit mask whose bit 0 is key `at`
-__device__ __forceinline__ uint32_t keep_bits(int at, int lo, int hi)
-{
-    const int a = max(0, lo - at), b = min(32, hi - at);
-    if (a >= b) return 0u;
-    return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAttnArgs A)
 {
@@ -710,15 +702,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                     __syncwarp();
                 }
                 float c0, c1;
-                bool fast;
+                bool plain, edge;
+                const int t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
                 {
                     const float4 b = ld_shared_f4(scales + 16 * (j % kWindow));  // of both blocks
-                    const int t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
                     c0 = rc * b.x;
                     c1 = rc * b.z;
-                    // else f is applied apart from the exponent
-                    fast = __all_sync(0xffffffffu, b.y > 1e-15f && b.y < INFINITY && b.w > 1e-15f && b.w < INFINITY &&
-                                                       lo <= t0 && hi >= t0 + 2 * kPage);
+                    // else f is applied apart from the exponent, and unseen keys need more than a score of -inf
+                    plain = __all_sync(0xffffffffu, b.y > 1e-15f && b.y < INFINITY && b.w > 1e-15f && b.w < INFINITY &&
+                                                        c0 > 0.0f && c0 < INFINITY && c1 > 0.0f && c1 < INFINITY);
+                    edge = __any_sync(0xffffffffu, lo > t0 || hi < t0 + 2 * kPage);
                 }
                 if (!wait(kBarSFull + t, c)) break;
                 uint32_t s[4][32];
@@ -728,14 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                 for (int k = 0; k < 4; ++k) regs_ready(s[k]);
-                if (!fast) {
-                    const int t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
+                if (edge) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t keep = keep_bits(t0 + 32 * k, lo, hi);
+                        const int first = lo - (t0 + 32 * k), end = hi - (t0 + 32 * k);
+                        if (!__any_sync(0xffffffffu, first > 0 || end < 32)) continue;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!((keep >> e) & 1u)) s[k][e] = kMinusInf;
+                            if (e < first || e >= end) s[k][e] = kMinusInf;
                     }
                 }
                 // the scales are not negative, so they commute with the maximum (0 * -inf is
@@ -757,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 tc_fence_after();
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const float4 b = ld_shared_f4(scales + 16 * (j % kWindow));
-                if (fast) {
+                if (plain) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t pw[16];
