@@ -549,8 +549,7 @@ __device__ __forceinline__ void load_floats(const float *p, float (&v)[2])
 }
 
 // Joins the pieces of the segments, of ROWS rows at most, that a worker began and others went on
-// with: workers blockIdx.x, blockIdx.x + gridDim.x, ..., of each segment the 16 rows blockIdx.y.  A
-// piece is acc [ROWS][D], m [ROWS], l [ROWS].  The warps take the rows, and share a row's pieces
+// with: workers blockIdx.x, blockIdx.x + gridDim.x, ....  A piece is acc [ROWS][D], m [ROWS], l [ROWS].  The warps take the rows, and share a row's pieces
 // where there are fewer rows.
 constexpr int kCombineWarps = 8, kCombineThreads = 32 * kCombineWarps;
 template <typename T, int D, int ROWS>
@@ -567,13 +566,11 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
         found &= found - 1;
         const int pieces = __shfl_sync(0xffffffffu, mine.x, k), slot0 = __shfl_sync(0xffffffffu, mine.y, k);
         const int4 where = A.meta[2 * w + 1];  // first token, head, row of the segment in its head, its rows
-        const int row0 = where.z + 16 * int(blockIdx.y), rows = min(16, where.w - 16 * int(blockIdx.y));
-        if (rows <= 0) continue;
+        const int row0 = where.z, rows = where.w;
         int groups = 1;
         while (groups < rows && groups < kCombineWarps) groups *= 2;
         const int subs = kCombineWarps / groups, sub = warp / groups;
         for (int r = warp % groups; r < (subs > 1 ? groups : rows); r += groups) {
-            const int rp = r + 16 * int(blockIdx.y);
             auto part_of = [&](int p) { return A.part + int64_t(p == 0 ? slot0 : 2 * (w + p)) * kPart; };
             // A lane adds up kPer neighbouring channels of a row, kBatch pieces in flight at a time; the
             // first batch is on its way while the weights are found.
@@ -588,8 +585,8 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
                     for (int e = 0; e < kPer; ++e) v[q][e] = 0.0f;
                     if (p < pieces && r < rows) {
                         const float *part = part_of(p);
-                        vm[q] = part[ROWS * D + rp];
-                        load_floats(part + rp * D + lane * kPer, v[q]);
+                        vm[q] = part[ROWS * D + r];
+                        load_floats(part + r * D + lane * kPer, v[q]);
                     }
                 }
             };
@@ -597,7 +594,7 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
 #pragma unroll
             for (int e = 0; e < kPer; ++e) out[e] = 0.0f;
             if (r < rows) {
-                for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + rp]);
+                for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + r]);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             }
@@ -605,7 +602,7 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
             if (r < rows) {
                 for (int p = lane; p < pieces; p += 32) {
                     const float *part = part_of(p);
-                    total += ex2_approx(part[ROWS * D + rp] - ref) * part[ROWS * (D + 1) + rp];
+                    total += ex2_approx(part[ROWS * D + r] - ref) * part[ROWS * (D + 1) + r];
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -648,7 +645,7 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
 template <typename T, int D, int ROWS>
 cudaError_t launch_combine(const CacheAttnArgs &a, int workers, int sms, cudaStream_t st)
 {
-    return launch_chained(cache_combine_kernel<T, D, ROWS>, dim3(unsigned(std::min(workers, 6 * sms)), unsigned(cdiv(ROWS, 16))),
+    return launch_chained(cache_combine_kernel<T, D, ROWS>, dim3(unsigned(std::min(workers, 6 * sms))),
                           kCombineThreads, 0, st, a, workers);
 }
 
@@ -667,10 +664,7 @@ cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const C
 template <typename T, int D>
 cudaError_t launch_any(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms, cudaStream_t st)
 {
-    if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) {
-        const cudaError_t e = launch_cache_chunk(a, sms, st);
-        return e == cudaSuccess ? launch_combine<T, D, 256>(a, sms, sms, st) : e;
-    }
+    if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) return launch_cache_chunk(a, sms, st);
     // two tiles of eight rows at once where most segments have more than eight
     if (int64_t(a.T) * a.G > int64_t(8) * a.B) return launch_for<T, D, 2>(tm_k, tm_v, a, sms, st);
     return launch_for<T, D, 1>(tm_k, tm_v, a, sms, st);

@@ -633,73 +633,95 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 hi = min(valid && A.causal ? pos + 1 : w.s.len, w.r.bhi * kPage);
                 lo = valid && A.window > 0 ? max(0, pos - A.window + 1) : 0;
             }
-            // ---- this row of q, fp16 (the tile is free: S of the last step before was read)
-            float rc;
+            // The scales are found a window of 16 steps at a time, the pages two windows and the scales one
+            // ahead; lane i has those of block i of the window.
+            auto page_at = [&](int j) {  // -1: no such block
+                const int blk = w.r.blo + 2 * (w.off + j) + lane;
+                return blk < w.r.bhi && 2 * j + lane < 2 * w.count ? A.table[int64_t(w.b) * A.max_pages + blk] : -1;
+            };
+            auto scales_at = [&](int j, int page, float &sk, float &sv) {
+                const int blk = w.r.blo + 2 * (w.off + j) + lane;
+                sk = sv = 0.0f;
+                if (!(blk < w.r.bhi && 2 * j + lane < 2 * w.count)) return;
+                sk = sv = __int_as_float(0x7fffffff);
+                if (page < 0 || page >= A.num_pages) return;
+                sk = A.k_scale[int64_t(page) * A.H + w.h];
+                sv = A.v_scale[int64_t(page) * A.H + w.h];
+            };
+            int page_n = page_at(0);
+            // ---- the rows of q, fp16 (the tile is free: S of the last step before was read).  A row takes kLanes
+            // lanes, 16 bytes each; all loads are in flight at once.
+            constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+            float rc, sk_n, sv_n;
             {
                 const int rr = w.p * kRowsSeg + t * 128 + row, i = rr / A.G;
-                const bool valid = rr < w.s.n * A.G;
-                const T *src = static_cast<const T *>(A.q) + (int64_t(w.s.ts) + i) * A.q_stride +
-                               int64_t(w.h * A.G + rr - i * A.G) * D;
-                uint4 x[D / 8];  // all loads in flight at once
+                const int64_t own = rr < w.s.n * A.G ? (int64_t(w.s.ts) + i) * A.q_stride + int64_t(w.h * A.G + rr - i * A.G) * D : -1;
+                uint4 x[kLanes];
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k) x[k] = valid ? *reinterpret_cast<const uint4 *>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-                float up = 1.0f, down = 1.0f;
-                if (A.dtype == 0) {
-                    uint32_t top = 0;  // maximum of the bits of |x|, two at a time
-#pragma unroll
-                    for (int k = 0; k < D / 8; ++k)
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
-                                                     __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
-                    row_power(__uint_as_float(max(top & 0xffffu, top >> 16) << 16), up, down);
+                for (int k = 0; k < kLanes; ++k) {
+                    const int64_t from = __shfl_sync(0xffffffffu, own, k * kAtOnce + lane / kLanes);
+                    x[k] = make_uint4(0, 0, 0, 0);
+                    if (from >= 0)
+                        x[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + from + 8 * (lane % kLanes));
                 }
-                rc = A.sm_scale * kLog2e * down;
+                scales_at(0, page_n, sk_n, sv_n);
+                page_n = page_at(kWindow);
+                uint32_t mine = 0;  // bits of the largest |q| of this thread's row
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k) {
+                for (int k = 0; k < kLanes; ++k) {
+                    const int r = wq * 32 + k * kAtOnce + lane / kLanes, chunk = lane % kLanes;
                     uint4 v = x[k];
                     if (A.dtype == 0) {
+                        uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+#pragma unroll
+                        for (int o = 1; o < kLanes; o *= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        top = max(top & 0xffffu, top >> 16);
+                        const uint32_t theirs = __shfl_sync(0xffffffffu, top, lane % kAtOnce * kLanes);
+                        mine = lane / kAtOnce == k ? theirs : mine;
+                        float up, down;
+                        row_power(__uint_as_float(top << 16), up, down);
                         uint32_t *w4 = &v.x;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             w4[e] = pack_h2(__uint_as_float(w4[e] << 16) * up, __uint_as_float(w4[e] & 0xffff0000u) * up);
                     }
-                    st_shared_v4(sbase + S::kOffQ + uint32_t(t) * S::kTileBytes + (k / 8) * S::kSubBytes + row * 128 +
-                                     (((k & 7) ^ (row & 7)) << 4),
+                    st_shared_v4(sbase + S::kOffQ + uint32_t(t) * S::kTileBytes + (chunk / 8) * S::kSubBytes + r * 128 +
+                                     (((chunk & 7) ^ (r & 7)) << 4),
                                  v);
                 }
+                float up, down = 1.0f;
+                if (A.dtype == 0) row_power(__uint_as_float(mine << 16), up, down);
+                rc = A.sm_scale * kLog2e * down;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarQFull + t));
             }
             float m = -INFINITY, l = 0.0f, u = 0.0f;
-            // The scales of 16 steps at a time go to shared memory, for each block scale_k and
-            // f = 2^5 scale_v / u.  The warps of both tiles write the same values, four windows in turn:
-            // no two warps are that far apart, for each S needs the one before it to have been read.
+            // The scales go to shared memory, for each block scale_k and f = 2^5 scale_v / u.  The warps of
+            // both tiles write the same values, four windows in turn: no two warps are that far apart,
+            // for each S needs the one before it to have been read.
             uint32_t scales = 0;
             for (int j = 0; j < w.count; ++j, ++c) {
                 float su = 1.0f;
                 if (j % kWindow == 0) {
                     scales = sbase + S::kOffScale + (turn++ % kWindows) * (2 * kWindow * 8);
                     const int blk = w.r.blo + 2 * (w.off + j) + lane;
-                    float sv = 0.0f, sk = 0.0f;
-                    if (blk < w.r.bhi && 2 * j + lane < 2 * w.count) {
-                        const int page = A.table[int64_t(w.b) * A.max_pages + blk];
-                        if (page < 0 || page >= A.num_pages) {
-                            sk = sv = __int_as_float(0x7fffffff);
-                        } else {
-                            sk = A.k_scale[int64_t(page) * A.H + w.h];
-                            sv = A.v_scale[int64_t(page) * A.H + w.h];
-                        }
-                    }
                     // the reference of the value scales; one that is not finite leaves it
                     const float top = __uint_as_float(
-                        __reduce_max_sync(0xffffffffu, sv > 0.0f && sv < INFINITY ? __float_as_uint(sv) : 0u));
+                        __reduce_max_sync(0xffffffffu, sv_n > 0.0f && sv_n < INFINITY ? __float_as_uint(sv_n) : 0u));
                     if (top > 4.0f * u) {
                         const float u_new = scale_ref(top);
                         su = u / u_new;
                         u = u_new;
                     }
-                    st_shared_f2(scales + 8 * lane, sk, sv == 0.0f ? 0.0f : 32.0f * (sv / u));
+                    if (blk < w.r.bhi)
+                        st_shared_f2(scales + 8 * lane, sk_n, sv_n == 0.0f ? 0.0f : 32.0f * (sv_n / u));
+                    else
+                        st_shared_f2(scales + 8 * lane, 1.0f, 32.0f);  // no such block: none of its keys is seen
                     __syncwarp();
+                    scales_at(j + kWindow, page_n, sk_n, sv_n);
+                    page_n = page_at(j + 2 * kWindow);
                 }
                 float c0, c1;
                 bool plain, edge;
@@ -831,10 +853,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                                            pack_out(fl_of(r[e + 4]) * f, fl_of(r[e + 5]) * f, T()),
                                            pack_out(fl_of(r[e + 6]) * f, fl_of(r[e + 7]) * f, T()));
                     } else {
-                        float *dst = part + int64_t(t * 128 + row) * D + 32 * k;
+                        float *dst = part + (8 * k * kRowsSeg + t * 128 + row) * 4;  // [D / 4][row][4]
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(dst + e) = make_float4(fl_of(r[e]) * f, fl_of(r[e + 1]) * f,
+                            *reinterpret_cast<float4 *>(dst + e * kRowsSeg) = make_float4(fl_of(r[e]) * f, fl_of(r[e + 1]) * f,
                                                                                fl_of(r[e + 2]) * f, fl_of(r[e + 3]) * f);
                     }
                 }
@@ -857,13 +879,61 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     if (warp == kWarpQK) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Joins the pieces of the segment that worker blockIdx.x began and others went on with, in the
+// order of the workers.  A piece is acc [D / 4][256][4], m [256], l [256]: a warp takes 32 rows, one
+// a lane, and 16 channels, so its reads are contiguous.
+constexpr int kCombineThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) cache_chunk_combine_kernel(const CacheAttnArgs A)
+{
+    constexpr int kPart = Sizes<D>::kPart, kGroups = kRowsSeg / 32;
+    chain_begin();
+    const int w = blockIdx.x, task = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5);
+    const int4 meta = A.meta[2 * w], where = A.meta[2 * w + 1];
+    const int row = task % kGroups * 32 + (threadIdx.x & 31), ch = task / kGroups * 16;
+    if (meta.x == 0 || row >= where.w) return;
+    auto part_of = [&](int p) { return A.part + int64_t(p == 0 ? meta.y : 2 * (w + p)) * kPart; };
+    float big = -INFINITY, total = 0.0f, out[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) out[e] = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < meta.x; ++p) big = fmaxf(big, part_of(p)[kRowsSeg * D + row]);
+    const float ref = big == -INFINITY ? 0.0f : big;
+#pragma unroll 2
+    for (int p = 0; p < meta.x; ++p) {
+        const float *part = part_of(p);
+        const float f = ex2_approx(part[kRowsSeg * D + row] - ref);
+        total = fmaf(f, part[kRowsSeg * (D + 1) + row], total);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(part + ((ch + e) / 4 * kRowsSeg + row) * 4);
+            out[e] = fmaf(f, v.x, out[e]);
+            out[e + 1] = fmaf(f, v.y, out[e + 1]);
+            out[e + 2] = fmaf(f, v.z, out[e + 2]);
+            out[e + 3] = fmaf(f, v.w, out[e + 3]);
+        }
+    }
+    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+    const int rr = where.z + row, i = rr / A.G;
+    const int64_t at = (int64_t(where.x) + i) * (A.H * A.G) + where.y * A.G + rr - i * A.G;
+    uint32_t y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = pack_out(out[2 * e] * f, out[2 * e + 1] * f, T());
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(A.o) + at * D + ch);
+    dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    if (A.lse && ch == 0) A.lse[at] = total == 0.0f ? -INFINITY : (big + log2f(total)) * kLn2;
+}
+
 template <typename T, int D>
 cudaError_t launch_for(const CacheAttnArgs &a, int sms, cudaStream_t st)
 {
     cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(Sizes<D>::kAlloc));
     if (e != cudaSuccess) return e;
-    return launch_chained(cache_chunk_kernel<T, D>, dim3(unsigned(sms)), kThreads, Sizes<D>::kAlloc, st, a);
+    e = launch_chained(cache_chunk_kernel<T, D>, dim3(unsigned(sms)), kThreads, Sizes<D>::kAlloc, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_chained(cache_chunk_combine_kernel<T, D>, dim3(unsigned(sms), D / 16), kCombineThreads, 0, st, a);
 }
 
 }  // namespace
