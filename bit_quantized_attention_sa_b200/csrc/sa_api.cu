@@ -1045,6 +1045,10 @@ sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T
     if ((r = check_tokens(q, q_tok, int64_t(H) * group * d)) != SA_OK) return r;
     if (!o || !workspace) return SA_ERR_INVALID_ARG;
     if (!aligned16(o) || !aligned16(workspace) || !aligned(lse, 4)) return SA_ERR_MISALIGNED;
+    // blocks that share a query row write it while others may still read it
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+    const int64_t width = int64_t(H) * group * d;
+    if (o0 < q0 + 2 * uint64_t((T - 1) * q_tok + width) && q0 < o0 + 2 * uint64_t(T * width)) return SA_ERR_INVALID_ARG;
     if ((r = check_device()) != SA_OK) return r;
     if (workspace_bytes < sa_cache_attn_workspace_bytes(T, B, H, group, d)) return SA_ERR_INVALID_ARG;
     CUtensorMap tm_k, tm_v;
@@ -1083,7 +1087,7 @@ size_t sa_cache_attn_workspace_bytes(int64_t T, int B, int H, int group, int d)
 {
     if (T < 0 || B < 1 || H < 1 || (d != 64 && d != 128) || check_group(T, H, group) != SA_OK) return 0;
     const int sms = device_sms();
-    return sms < 1 ? 0 : cache_attn_workspace(sms, d);
+    return sms < 1 ? 0 : cache_attn_workspace(sms, T, B, group, d);
 }
 
 sa_status sa_debug_qk_s32(const int8_t *q_i8, const int8_t *k_i8, int B, int H, int N, int d,

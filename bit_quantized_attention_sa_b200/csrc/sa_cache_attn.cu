@@ -39,9 +39,11 @@ __device__ int g_cache_attn_status;  // 0 = OK, 6 = a bounded wait expired, 8 = 
 
 namespace {
 
-// Rows of a sequence and head, on average, up to which this kernel takes a call; the others go
-// to the tensor-core kernel of sa_cache_chunk.cu.
-constexpr int kFewRows = 32;
+// Rows of a sequence and head, on average, up to which this kernel takes a call; the others go to
+// the tensor-core kernel of sa_cache_chunk.cu.  Measured at d = 128, 8 heads (this kernel / that
+// one, us): 16 rows, 16 sequences of 4000 tokens 50 / 70, 64 of them 140 / 234, one of 60000
+// 70 / 76; 24 rows, which are read twice here: 78 / 71, 252 / 237, 85 / 77.
+constexpr int kFewRows = 16;
 constexpr float kPScale = 16384.0f;
 
 // D: head size; NT: tiles of eight rows that a warp works on at once.  One tile leaves registers
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         row0 = (sg - head * sq.tiles) * kRows;
         const int rows = sq.n * A.G, pos0 = sq.len - sq.n;
         auto first_of = [&](int i) { return A.window > 0 ? max(0, pos0 + i - A.window + 1) : 0; };
-        auto last_of = [&](int i) { return A.causal ? pos0 + i : sq.len - 1; };
+        auto last_of = [&](int i) { return A.causal || pos0 + i < 0 ? pos0 + i : sq.len - 1; };
         const int i_lo = row0 / A.G, i_hi = min(rows - 1, row0 + kRows - 1) / A.G;
         tile_first = first_of(i_lo);
         all_first = first_of(i_hi);
@@ -649,6 +651,20 @@ cudaError_t launch_combine(const CacheAttnArgs &a, int workers, int sms, cudaStr
                           kCombineThreads, 0, st, a, workers);
 }
 
+size_t meta_bytes(int sms) { return (size_t(sms) * kMaxWarps * 2 * sizeof(int4) + 255) & ~size_t(255); }
+
+bool many_rows(int64_t T, int B, int G) { return B <= kCacheChunkMaxSeqs && T * G > int64_t(kFewRows) * B; }
+bool two_tiles(int64_t T, int B, int G) { return T * G > int64_t(8) * B; }  // where most segments have over eight rows
+
+template <int D>
+size_t part_bytes(int sms, int64_t T, int B, int G)
+{
+    if (many_rows(T, B, G)) return cache_chunk_part_bytes(sms, D);
+    const size_t each = two_tiles(T, B, G) ? size_t(Sizes<D, 2>::kWarps) * Sizes<D, 2>::kPart
+                                           : size_t(Sizes<D, 1>::kWarps) * Sizes<D, 1>::kPart;
+    return size_t(2) * sms * each * 4;
+}
+
 template <typename T, int D, int NT>
 cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms, cudaStream_t st)
 {
@@ -664,26 +680,16 @@ cudaError_t launch_for(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const C
 template <typename T, int D>
 cudaError_t launch_any(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CacheAttnArgs &a, int sms, cudaStream_t st)
 {
-    if (a.B <= kCacheChunkMaxSeqs && int64_t(a.T) * a.G > int64_t(kFewRows) * a.B) return launch_cache_chunk(a, sms, st);
-    // two tiles of eight rows at once where most segments have more than eight
-    if (int64_t(a.T) * a.G > int64_t(8) * a.B) return launch_for<T, D, 2>(tm_k, tm_v, a, sms, st);
+    if (many_rows(a.T, a.B, a.G)) return launch_cache_chunk(a, sms, st);
+    if (two_tiles(a.T, a.B, a.G)) return launch_for<T, D, 2>(tm_k, tm_v, a, sms, st);
     return launch_for<T, D, 1>(tm_k, tm_v, a, sms, st);
-}
-
-size_t meta_bytes(int sms) { return (size_t(sms) * kMaxWarps * 2 * sizeof(int4) + 255) & ~size_t(255); }
-
-template <int D>
-size_t part_bytes(int sms)
-{
-    const size_t one = size_t(Sizes<D, 1>::kWarps) * Sizes<D, 1>::kPart, two = size_t(Sizes<D, 2>::kWarps) * Sizes<D, 2>::kPart;
-    return std::max(size_t(2) * sms * std::max(one, two) * 4, cache_chunk_part_bytes(sms, D));
 }
 
 }  // namespace
 
-size_t cache_attn_workspace(int sms, int d)
+size_t cache_attn_workspace(int sms, int64_t T, int B, int G, int d)
 {
-    return meta_bytes(sms) + (d == 128 ? part_bytes<128>(sms) : part_bytes<64>(sms));
+    return meta_bytes(sms) + (d == 128 ? part_bytes<128>(sms, T, B, G) : part_bytes<64>(sms, T, B, G));
 }
 
 cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,

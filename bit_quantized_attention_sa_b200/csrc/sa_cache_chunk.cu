@@ -88,7 +88,7 @@ __device__ __forceinline__ Reach reach_of(const CacheAttnArgs &A, const Seq &s, 
 {
     const int rows = s.n * A.G, pos0 = s.len - s.n;
     const int i_lo = p * kRowsSeg / A.G, i_hi = min(rows - 1, p * kRowsSeg + kRowsSeg - 1) / A.G;
-    const int last = A.causal ? pos0 + i_hi : s.len - 1;
+    const int last = A.causal || pos0 + i_hi < 0 ? pos0 + i_hi : s.len - 1;
     const int first = A.window > 0 ? max(0, pos0 + i_lo - A.window + 1) : 0;
     Reach r;
     r.blo = first / kPage;
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
             {
                 const int rr = w.p * kRowsSeg + t * 128 + row, pos = w.s.len - w.s.n + rr / A.G;
                 const bool valid = rr < w.s.n * A.G;
-                hi = min(valid && A.causal ? pos + 1 : w.s.len, w.r.bhi * kPage);
+                hi = min(valid && (A.causal || pos < 0) ? pos + 1 : w.s.len, w.r.bhi * kPage);
                 lo = valid && A.window > 0 ? max(0, pos - A.window + 1) : 0;
             }
             // The scales are found a window of 16 steps at a time, the pages two windows and the scales one

@@ -188,7 +188,7 @@ struct CacheAttnArgs {
     int4 *meta = nullptr;
     float *part = nullptr;
 };
-size_t cache_attn_workspace(int sms, int d);
+size_t cache_attn_workspace(int sms, int64_t T, int B, int G, int d);
 // tm_k, tm_v: the codes as 128-byte lines, a box of one head's page, 128-byte swizzle
 cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
                               cudaStream_t st);

@@ -370,7 +370,7 @@ sa_status sa_cache_read(void *k, void *v, int dtype, int64_t T, const int32_t *t
  * over the cache, whose tokens include the queries' own (append first).  Query head h reads
  * key/value head h / group.  The query at position p sees the tokens t < kv_lens[b] with
  * t <= p (causal != 0) and t > p - window (window > 0; 0: no window).
- *   o [T, H * group, d] (contiguous, dtype) = sum_t softmax_t(q . k_t * sm_scale) v_t, and lse
+ *   o [T, H * group, d] (contiguous, dtype, apart from q in memory) = sum_t softmax_t(q . k_t * sm_scale) v_t, and lse
  *   fp32 [T, H * group] (or NULL) = log sum_t exp(q . k_t * sm_scale); a query that sees
  *   nothing has o = 0 and lse = -inf.
  * Products of fp16 operands (the codes and, up to a power of two for each row, q are exact;

@@ -83,7 +83,7 @@ def attn_ref(cache, q, starts, lens, table, causal=True, window=0, sm_scale=None
         t = torch.arange(length, device=q.device)
         page, slot = table[b].long()[t // PAGE], t % PAGE
         p = torch.arange(length - n, length, device=q.device)[:, None]
-        sees = torch.ones(n, length, dtype=torch.bool, device=q.device) & (p >= 0 if causal else p > -10 ** 12)
+        sees = torch.ones(n, length, dtype=torch.bool, device=q.device) & (p >= 0)
         if causal:
             sees &= t <= p
         if window > 0:

@@ -47,7 +47,7 @@ def test_read_refusals(libsa, kw, expect):
 
 
 def _attn(lib, **kw):
-    a = dict(q=FAKE, o=FAKE, lse=None, dtype=0, T=8, qs=2048, starts=FAKE, lens=FAKE, table=FAKE, B=2, max_pages=4,
+    a = dict(q=FAKE, o=FAKE + (1 << 24), lse=None, dtype=0, T=8, qs=2048, starts=FAKE, lens=FAKE, table=FAKE, B=2, max_pages=4,
              kc=FAKE, kscale=FAKE, vc=FAKE, vscale=FAKE, pages=16, H=8, group=2, d=128, causal=1, window=0, scale=SCALE,
              ws=FAKE, nbytes=1 << 40)
     a.update(kw)
@@ -57,11 +57,20 @@ def _attn(lib, **kw):
 @pytest.mark.parametrize("kw,expect", [
     (dict(q=None), 1), (dict(o=None), 1), (dict(ws=None), 1), (dict(dtype=2), 1), (dict(group=0), 1), (dict(window=-1), 1),
     (dict(scale=ctypes.c_float(0.0)), 1), (dict(scale=ctypes.c_float(math.nan)), 1), (dict(scale=ctypes.c_float(math.inf)), 1),
-    (dict(qs=2040), 1), (dict(d=80), 2), (dict(group=8192), 2), (dict(T=1 << 30), 2), (dict(o=ODD), 3), (dict(ws=ODD), 3),
+    (dict(qs=2040), 1), (dict(d=80), 2), (dict(group=8192), 2), (dict(T=1 << 30), 2), (dict(o=ODD), 3), (dict(ws=ODD), 3), (dict(o=FAKE), 1),
     (dict(lse=FAKE + 2), 3), (dict(qs=2052), 3), (dict(T=0, q=None, o=None, ws=None), 0),
 ])
 def test_attn_refusals(libsa, kw, expect):
     assert _attn(libsa.raw_library(), **kw) == expect
+
+
+def test_attn_refuses_an_output_over_its_queries(libsa):
+    """T tokens of H * group * d = 2048 values with a stride of 4096: outputs that reach the first
+    or the last 16 bytes of the span of q."""
+    lib, T = libsa.raw_library(), 8
+    span, size = 2 * ((T - 1) * 4096 + 2048), 2 * T * 2048
+    for o in (FAKE - size + 16, FAKE, FAKE + span - 16):
+        assert _attn(lib, q=FAKE, o=o, qs=4096) == 1
 
 
 def test_attn_workspace_of_refused_sizes_is_zero(libsa):

@@ -56,8 +56,9 @@ def test_rows_that_see_nothing(libsa, cuda_ok, new):
     news, lens = [new, new, 0, new, new], [0, 130, 64, max(0, new - 3), 0]
     cache, q, starts, dlens, table = _case(7, news, [max(n, 1) for n in lens], H, G, d, torch.bfloat16)
     dlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    check_attn(libsa.sa_cache_attn(cache, q, starts, dlens, table, return_lse=True),
-               attn_ref(cache, q, starts, dlens, table), torch.bfloat16)
+    for kw in (dict(), dict(causal=False), dict(causal=False, window=20)):
+        check_attn(libsa.sa_cache_attn(cache, q, starts, dlens, table, return_lse=True, **kw),
+                   attn_ref(cache, q, starts, dlens, table, **kw), torch.bfloat16)
     wide = torch.cat([q[:3], q, torch.cat([q, q])[:5]])  # 3 rows before, 5 behind
     out = torch.full((wide.shape[0], H * G, d), 9.0, device="cuda", dtype=torch.bfloat16)
     libsa.sa_cache_attn(cache, wide, starts + 3, dlens, table, out=out)
@@ -116,6 +117,43 @@ def test_many_sequences_and_few_blocks(libsa, cuda_ok):
     gen = torch.Generator().manual_seed(61)
     lens = [int(n) for n in torch.randint(1, 200, (600,), generator=gen)]
     _run(libsa, _case(62, [1] * 600, lens, 1, 2, 64, torch.bfloat16), torch.bfloat16)
+
+
+@pytest.mark.parametrize("B", [65, 300, 1500])
+def test_many_short_chunks(libsa, cuda_ok, B):
+    """Many sequences of some tokens each, empty ones among them."""
+    gen = torch.Generator().manual_seed(B)
+    new = [int(n) for n in torch.randint(0, 60, (B,), generator=gen)]
+    lens = [n + int(m) for n, m in zip(new, torch.randint(0, 90, (B,), generator=gen))]
+    cache, q, starts, _, table = _case(63, new, [max(1, n) for n in lens], 1, 2, 64, torch.float16)
+    _run(libsa, (cache, q, starts, torch.tensor(lens, dtype=torch.int32, device="cuda"), table), torch.float16)
+
+
+@pytest.mark.parametrize("n", [8, 9, 15, 16, 17, 33])
+def test_rows_around_the_tiles(libsa, cuda_ok, n):
+    """Row counts at which another kernel, or another number of tiles, takes over."""
+    for G in (1, 2):
+        _run(libsa, _case(64 + n, [n, n], [200, 1333], 2, G, 128, torch.bfloat16), torch.bfloat16)
+
+
+def test_output_over_the_queries_is_refused(libsa, cuda_ok):
+    cache, q, starts, lens, table = _case(65, [1, 1], [100, 200], 2, 2, 128, torch.bfloat16)
+    with pytest.raises(libsa.SAError) as e:
+        libsa.sa_cache_attn(cache, q, starts, lens, table, out=q)
+    assert e.value.status == 1
+
+
+def test_non_finite_queries_stay_in_their_row(libsa, cuda_ok):
+    for new in (3, 150):
+        cache, q, starts, lens, table = _case(66, [new], [400], 1, 2, 128, torch.bfloat16)
+        clean = libsa.sa_cache_attn(cache, q, starts, lens, table)
+        bad = q.clone()
+        bad[1, 0, 5], bad[2, 1, 7] = math.nan, math.inf
+        got = libsa.sa_cache_attn(cache, bad, starts, lens, table)
+        assert torch.isnan(got[1, 0]).all()
+        same = torch.ones(new, 2, dtype=torch.bool, device="cuda")
+        same[1, 0] = same[2, 1] = False
+        assert torch.equal(got[same], clean[same])
 
 
 def test_one_long_sequence(libsa, cuda_ok):
