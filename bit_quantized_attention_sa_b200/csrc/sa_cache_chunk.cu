@@ -45,8 +45,7 @@ constexpr int kThreads = 512;
 constexpr int kWarpConvert = 8, kWarpQK = 12, kWarpPV = 13;
 constexpr int kStages = 4;  // fp16 tiles
 constexpr int kRaw = 2;     // tiles of codes on their way
-constexpr int kWindow = 16;  // steps whose scales are in shared memory, in kWindows turns
-constexpr int kWindows = 4;
+constexpr int kWindow = 16;  // steps whose scales are in shared memory, two windows in turn for each tile
 constexpr int kRowsSeg = 256;
 constexpr uint32_t kTmemCols = 512, kColS = 0;
 __host__ __device__ constexpr uint32_t col_p(int t) { return 128u + 64u * uint32_t(t); }
@@ -155,7 +154,7 @@ struct Sizes {
     static constexpr uint32_t kRawBytes = 128 * D;
     static constexpr uint32_t kOffRaw = kOffKv + kStages * kTileBytes;
     static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawBytes;
-    static constexpr uint32_t kOffBar = kOffScale + kWindows * 2 * kWindow * 8;
+    static constexpr uint32_t kOffBar = kOffScale + 2 * 2 * 2 * kWindow * 8;
     static constexpr uint32_t kOffWalk = kOffBar + 8 * (kNumBars + 1);
     static constexpr uint32_t kOffMisc = kOffWalk + uint32_t(sizeof(Walk)) * (kWarpPV + 1);
     static constexpr uint32_t kAlloc = kOffMisc + 48;  // range, first, tensor memory's address, abort flag
@@ -622,10 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
         bool split = false;
         const int wk = int(blockIdx.x);
         for (; w.open(A); w.next(A)) {
-            if (t >= w.tiles(A)) {
-                turn += (w.count + kWindow - 1) / kWindow;
-                continue;
-            }
+            if (t >= w.tiles(A)) continue;
             int lo, hi;  // the keys that this row sees, [lo, hi); rows past the last see all, and are not written
             {
                 const int rr = w.p * kRowsSeg + t * 128 + row, pos = w.s.len - w.s.n + rr / A.G;
@@ -698,14 +694,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 if (lane == 0) mbar_arrive(bar(kBarQFull + t));
             }
             float m = -INFINITY, l = 0.0f, u = 0.0f;
-            // The scales go to shared memory, for each block scale_k and f = 2^5 scale_v / u.  The warps of
-            // both tiles write the same values, four windows in turn: no two warps are that far apart,
-            // for each S needs the one before it to have been read.
+            // The scales go to shared memory, for each block scale_k and f = 2^5 scale_v / u.  The four warps
+            // of the tile write the same values, two windows in turn: none is further than into its next
+            // window while another reads the one before, for each S needs all four to have read the last.
             uint32_t scales = 0;
             for (int j = 0; j < w.count; ++j, ++c) {
                 float su = 1.0f;
                 if (j % kWindow == 0) {
-                    scales = sbase + S::kOffScale + (turn++ % kWindows) * (2 * kWindow * 8);
+                    scales = sbase + S::kOffScale + uint32_t(2 * t + (turn++ & 1)) * (2 * kWindow * 8);
                     const int blk = w.r.blo + 2 * (w.off + j) + lane;
                     // the reference of the value scales; one that is not finite leaves it
                     const float top = __uint_as_float(

@@ -48,6 +48,17 @@ def test_long_chunks(libsa, cuda_ok, G):
     _run(libsa, _case(G, new, lens, 2, G, 128, torch.float16), torch.float16)
 
 
+@pytest.mark.parametrize("n,G,H,L", [(280, 1, 6, 16000), (70, 4, 6, 16000), (390, 2, 6, 9001), (280, 1, 48, 20000)])
+def test_last_rows_over_long_caches(libsa, cuda_ok, n, G, H, L):
+    """Chunks whose last rows fill less than half of a segment, between whole ones, over caches of
+    many steps, in the last case over a hundred for each SM; the same every time."""
+    case = _case(n + H, [n], [L], H, G, 128, torch.bfloat16)
+    first = _run(libsa, case, torch.bfloat16, causal=False)
+    for _ in range(5):
+        again = libsa.sa_cache_attn(*case, causal=False, return_lse=True)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 @pytest.mark.parametrize("new", [1, 90])
 def test_rows_that_see_nothing(libsa, cuda_ok, new):
     """Idle sequences, tokens before their sequence, empty pieces, rows before the first and
@@ -159,6 +170,23 @@ def test_non_finite_queries_stay_in_their_row(libsa, cuda_ok):
 def test_one_long_sequence(libsa, cuda_ok):
     _run(libsa, _case(71, [1], [70001], 2, 4, 128, torch.bfloat16), torch.bfloat16)
     _run(libsa, _case(72, [1, 1], [40000, 5], 1, 16, 64, torch.float16), torch.float16, window=30000)
+
+
+@pytest.mark.parametrize("G", [2, 16])
+def test_many_blocks_for_each_warp(libsa, cuda_ok, G):
+    """So many cached tokens that every warp of the GPU has over 64 blocks, in several segments."""
+    H, d, B, L = 8, 64, 9, 120000
+    gen = torch.Generator("cuda").manual_seed(73)
+    lens = [L - 977 * i for i in range(B)]
+    pages = sum(-(-n // 64) for n in lens)
+    assert pages * H > 64 * 148 * 12
+    cache = [torch.randint(-127, 128, (pages, H, 64, d), generator=gen, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scale = [torch.rand((pages, H), generator=gen, device="cuda") * 0.04 + 0.005 for _ in range(2)]
+    table = random_table(torch.Generator().manual_seed(74), lens, pages)
+    q = torch.randn(B, H * G, d, generator=gen, device="cuda").bfloat16()
+    case = ((cache[0], scale[0], cache[1], scale[1]), q, starts_of([1] * B),
+            torch.tensor(lens, dtype=torch.int32, device="cuda"), table)
+    _run(libsa, case, torch.bfloat16)
 
 
 def test_strided_queries_of_a_fused_projection(libsa, cuda_ok):
