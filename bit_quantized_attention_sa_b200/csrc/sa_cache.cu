@@ -47,7 +47,8 @@ template <int kThreads>
 __device__ __forceinline__ bool find_place(const CacheArgs &A, int slot, Place &P)
 {
     // base is increasing in b: b is the last one whose base is at or below the slot; the thread
-    // that looks at it has the rest of what there is to know already on its way
+    // that looks at it has the rest of what there is to know already on its way.  Where offsets
+    // decrease, the count names some other sequence, which finds that the slot is not its own.
     __shared__ int found[4];
     int below = 0;
     for (int i = 0; i < A.B; i += kThreads) {
@@ -60,7 +61,7 @@ __device__ __forceinline__ bool find_place(const CacheArgs &A, int slot, Place &
         }
         const bool in = b < A.B && ts / kPage + 2 * b <= slot;
         const int c = __syncthreads_count(in);
-        if (in && int(threadIdx.x) == c - 1) {
+        if (int(threadIdx.x) == c - 1) {
             found[0] = b;
             found[1] = ts;
             found[2] = te;

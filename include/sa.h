@@ -297,7 +297,8 @@ sa_status sa_sla_fwd(const void *q, const void *k, const void *v, void *o, int B
  *     changes.  One that is out of range (page outside [0, num_pages), length above
  *     64 * max_pages, offsets that decrease or pass T) sets SA_ERR_BAD_INDEX in the device
  *     status word: nothing is stored through it, a bad page reads as NaN, and a sequence whose
- *     length or offsets are bad is left out, its output rows as they were.
+ *     length or offsets are bad is left out, its output rows as they were (appending and
+ *     reading may leave out others beside offsets that decrease).
  *   - T = 0 (N = 0) is a valid call that does nothing.
  *   - The codes, k, v, q, o, x, y and the workspace are 16-byte aligned; freqs 8-byte; the int32
  *     and the other fp32 arrays 4-byte.  Token strides are in elements, multiples of 16 bytes, and at
@@ -325,7 +326,8 @@ sa_status sa_rope_frequencies(int rot, double base, int scaling, double factor, 
 
 /* One tensor of a rotation: x -> y, [B, heads, N, d] by element strides of batch, head and
  * token (channels contiguous).  y == x with equal strides rotates in place; x and y must not
- * overlap in any other way. */
+ * overlap in any other way, nor y's elements each other (a stride of 0 over more than one is
+ * refused). */
 typedef struct {
     const void *x;
     void *y;
@@ -372,7 +374,7 @@ sa_status sa_cache_read(void *k, void *v, int dtype, int64_t T, const int32_t *t
  * t <= p (causal != 0) and t > p - window (window > 0; 0: no window).
  *   o [T, H * group, d] (contiguous, dtype, apart from q in memory) = sum_t softmax_t(q . k_t * sm_scale) v_t, and lse
  *   fp32 [T, H * group] (or NULL) = log sum_t exp(q . k_t * sm_scale); a query that sees
- *   nothing has o = 0 and lse = -inf.
+ *   nothing has o = 0 and lse = -inf.  sm_scale is positive and finite.
  * Products of fp16 operands (the codes and, up to a power of two for each row, q are exact;
  * softmax weights are rounded to fp16), sums and statistics in fp32.  The result does not
  * depend on timing.  workspace: device memory of at least

@@ -191,6 +191,43 @@ def test_bad_pages_lengths_and_offsets_are_reported(libsa, cuda_ok):
     assert libsa.sa_get_device_status() == 8
 
 
+@pytest.mark.parametrize("tokens,B", [(150, 3), (20, 20)])
+def test_offsets_out_of_order_are_reported(libsa, cuda_ok, tokens, B):
+    """Offsets that jump ahead and back: the sequence beside the jump is reported and not stored,
+    pages of no sequence stay as they were."""
+    gen = torch.Generator().manual_seed(17)
+    H, d, pages = 2, 128, 2 * B + 4
+    x = torch.randn(tokens, H, d, generator=gen).cuda().bfloat16()
+    table = torch.arange(2 * B, dtype=torch.int32, device="cuda").reshape(B, 2)
+    lens = torch.full((B,), 128, dtype=torch.int32, device="cuda")
+    for ahead in (10 ** 9, -10 ** 9, 100000):
+        starts = torch.linspace(0, tokens, B + 1).to(torch.int32)
+        starts[B // 2] = ahead
+        starts = starts.cuda()
+        cache = random_cache(gen, pages, H, d)
+        was = [t.clone() for t in cache]
+        libsa.sa_cache_append(cache, x, x, starts, lens, table)
+        assert libsa.sa_get_device_status() == 8
+        for t, w in zip(cache, was):
+            assert torch.equal(t[2 * (B // 2):2 * (B // 2) + 2], w[2 * (B // 2):2 * (B // 2) + 2])
+            assert torch.equal(t[2 * B:], w[2 * B:])
+        libsa.sa_cache_read(cache, tokens, starts, lens, table)
+        assert libsa.sa_get_device_status() == 8
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_one_sequence_brings_all_the_tokens(libsa, cuda_ok, dtype):
+    """A batch of few tokens on average, of which one sequence has all: over many blocks."""
+    gen = torch.Generator().manual_seed(18)
+    H, d, B = 3, 128, 80
+    new = [0] * B
+    new[33] = 300
+    lens = [n + (7 * i) % 70 for i, n in enumerate(new)]
+    cache, table = random_cache(gen, 160, H, d), random_table(gen, lens, 160)
+    k, v = (torch.randn(300, H, d, generator=gen).cuda().to(dtype) for _ in range(2))
+    _append_and_check(libsa, cache, k, v, new, lens, table)
+
+
 def test_nothing_to_do(libsa, cuda_ok):
     cache = libsa.sa_cache_alloc(2, 2, 64)
     x = torch.zeros(0, 2, 64, device="cuda", dtype=torch.bfloat16)
