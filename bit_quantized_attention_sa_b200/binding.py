@@ -472,7 +472,8 @@ def sa_rope(q, k, pos, freqs, rot: int | None = None, interleaved: bool = False,
     tokens, not their head count.  pos int32 [N], [B, N] or [T]; with sections (pair counts of
     2 to 4 axes, or 1) it has the axes in front.  freqs fp64 [rot / 2] and amplitude as from
     sa_rope_frequencies; rot defaults to d.  inverse turns back (times amplitude): the
-    transposed map.  out: (q', k') or q' to write, which may be the inputs themselves.
+    transposed map.  out: (q', k') or q' to write, which may be the inputs themselves and must
+    not overlap them otherwise.
     Returns (q', k'), or q' without k."""
     out_q = out_k = None
     if out is not None:
@@ -492,7 +493,8 @@ def sa_cache_append(cache, k, v, tok_start, kv_lens, page_table) -> None:
 
 def sa_cache_read(cache, tokens: int, tok_start, kv_lens, page_table, dtype=torch.bfloat16):
     """The values (k, v), each [tokens, heads, d] of dtype (bf16, fp16 or fp32), of the tokens
-    at tok_start / kv_lens: the last tok_start[b + 1] - tok_start[b] of each sequence."""
+    at tok_start / kv_lens: the last tok_start[b + 1] - tok_start[b] of each sequence.  Rows that
+    belong to no sequence are not written."""
     return _sa_torch.read(*cache, tokens, tok_start, kv_lens, page_table, dtype)
 
 
@@ -503,7 +505,8 @@ def sa_cache_attn(cache, q, tok_start, kv_lens, page_table, causal: bool = True,
     position p sees the tokens t < kv_lens[b] with t <= p (causal) and t > p - window (if
     window > 0).  The query heads are a multiple of the cache's heads; heads that follow each
     other share one.  Returns o [T, query heads, d], and lse fp32 [T, query heads] with
-    return_lse; 0 and -inf for a query that sees nothing."""
+    return_lse; 0 and -inf for a query that sees nothing.  Rows that belong to no sequence are
+    not written."""
     return _sa_torch.attn(*cache, q, tok_start, kv_lens, page_table, causal, window, sm_scale, return_lse, out)
 
 

@@ -940,6 +940,8 @@ sa_status sa_rope(const sa_rope_tensor *tensors, int count, int dtype, int B, in
         if (!aligned16(t.x) || !aligned16(t.y)) return SA_ERR_MISALIGNED;
         for (int64_t st : {t.x_batch, t.x_head, t.x_tok, t.y_batch, t.y_head, t.y_tok})
             if (st % per16 != 0) return SA_ERR_MISALIGNED;
+        // an output that is its own copy would be turned several times in place
+        if ((B > 1 && t.y_batch == 0) || (t.heads > 1 && t.y_head == 0) || (N > 1 && t.y_tok == 0)) return SA_ERR_INVALID_ARG;
         a.io[i] = RopeIo{t.x, t.y, t.x_batch, t.x_head, t.x_tok, t.y_batch, t.y_head, t.y_tok, t.heads};
     }
     if (!pos || !freqs) return SA_ERR_INVALID_ARG;

@@ -105,6 +105,13 @@ def test_rope_refusals(libsa, kw, expect):
     assert _rope(libsa.raw_library(), **kw) == expect
 
 
+@pytest.mark.parametrize("kw", [dict(y_head=0), dict(y_tok=0), dict(B=2)])
+def test_rope_refuses_an_output_over_itself(libsa, kw):
+    # such an output would be read again after it was turned; broadcast inputs and sizes of one are fine
+    assert _rope(libsa.raw_library(), **kw) == 1
+    assert _rope(libsa.raw_library(), x_head=0, x_tok=0, y_head=0, y_tok=0, B=0) == 0
+
+
 def test_binding_refusals(libsa):
     x = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
     cache = tuple(libsa.sa_cache_alloc(4, 2, 128, device="cpu"))
