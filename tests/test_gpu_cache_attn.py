@@ -279,6 +279,47 @@ def test_captured_steps_follow_lengths(libsa, cuda_ok):
     assert libsa.sa_get_device_status() == 0
 
 
+def test_captured_on_two_streams_that_join(libsa, cuda_ok):
+    """A capture that forks to a second stream and joins: calls on both, one after the join that
+    needs what both wrote, and what torch runs in between."""
+    gen = torch.Generator().manual_seed(115)
+    H, d, n = 2, 128, 40
+    table = random_table(gen, [n, n], 4)
+    starts, lens = starts_of([n, n]), torch.tensor([n, n], dtype=torch.int32, device="cuda")
+    freqs, _ = libsa.sa_rope_frequencies(d)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").repeat(2)
+    q, k, v = (torch.zeros(2 * n, H, d, device="cuda", dtype=torch.float16) for _ in range(3))
+    cache = libsa.sa_cache_alloc(4, H, d)
+    side = torch.cuda.Stream()
+
+    def both(two):
+        here = torch.cuda.current_stream()
+        there = side if two else here
+        there.wait_stream(here)
+        with torch.cuda.stream(there):
+            rk = libsa.sa_rope(k, None, pos, freqs)
+            libsa.sa_cache_append(cache, rk, v, starts, lens, table)
+        rq = libsa.sa_rope(q, None, pos, freqs)
+        here.wait_stream(there)
+        o = libsa.sa_cache_attn(cache, rq, starts, lens, table)
+        return libsa.sa_rope(o * 2, None, pos, freqs, inverse=True), rk, rq
+
+    for t in (q, k, v):
+        t.copy_(torch.randn(t.shape, generator=gen))
+    both(False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(True)
+    for _ in range(20):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=gen))
+        graph.replay()
+        got = out[0].clone()
+        assert torch.equal(got, both(False)[0])
+    assert libsa.sa_get_device_status() == 0
+
+
 def test_two_streams_at_once(libsa, cuda_ok):
     """Calls in flight on two streams have workspaces of their own."""
     cases = [_case(121 + i, [1] * 8, [5000 + 100 * i] * 8, 4, 4, 128, torch.bfloat16) for i in range(2)]
