@@ -242,6 +242,12 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
     float row_c[NT][2], m[NT][2], l[NT][2], acc[NT][kMT][4], u_ref = 0.0f;
     int row_first[NT][2], row_last[NT][2];
 
+    auto arrived = [&]() -> const uint8_t * {
+        ok = mbar_wait(bars + 8 * uint32_t(done % kSlots), uint32_t(done / kSlots) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        return ring + (done % kSlots) * S::kTile;
+    };
+
     auto open_segment = [&](int b, int sg) {
         if (b != seg_b) sq = load_seq(A, b, kRows);
         head = sg / sq.tiles;
@@ -379,11 +385,10 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         const bool full = t0 >= all_first && t0 + kPage - 1 <= all_last;
 
         // ---- S^T = k8 . q: 16 keys by 8 rows a product
-        ok = mbar_wait(bars + 8 * uint32_t(done % kSlots), uint32_t(done / kSlots) & 1u, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         float s[NT][4][4];
+        const uint8_t *tile = arrived();
+        if (!ok) break;
         if (seen) {
-            const uint8_t *tile = ring + (done % kSlots) * S::kTile;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
@@ -477,10 +482,9 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         }
 
         // ---- acc^T += v8^T . P^T: 16 channels by 8 rows a product
-        ok = mbar_wait(bars + 8 * uint32_t(done % kSlots), uint32_t(done / kSlots) & 1u, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tile = arrived();
+        if (!ok) break;
         if (seen) {
-            const uint8_t *tile = ring + (done % kSlots) * S::kTile;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {  // 16 keys
                 uint32_t vw[4][D / 32];       // 4 keys x D / 8 channels of this lane
