@@ -341,7 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = reinterpret_cast<int *>(smem + S::kOffMisc + 36);
     if (sbase & 1023u) {  // never so far; the tiles would be read wrongly
-        if (threadIdx.x == 0) record(6);
+        chain_begin();
+        if (threadIdx.x == 0) {
+            record(6);
+            A.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);  // nothing to join
+        }
         return;
     }
     auto bar = [&](int i) -> uint32_t { return sbase + S::kOffBar + 8u * uint32_t(i); };
