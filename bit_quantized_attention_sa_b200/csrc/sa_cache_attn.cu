@@ -13,7 +13,9 @@
 // fp16, 2^14 times itself: at most 2^15, relative error 2^-11, and what is below 2^-28 of the
 // row's largest weight falls to fp16's subnormals.  acc is kept in units of u * 2^-14.
 //
-// What bounds it: reading 2 d bytes for each cached token and head.  So every warp is a worker
+// What bounds it: reading 2 d bytes for each cached token and head.  Measured, 4 sequences of
+// 70001 to 131072 tokens, 32 query heads on 8 of 128: 154 us for 900 MB, 5.9 TB/s (a plain copy
+// has 6.55), and 12 for the joining, some of it hidden.  So every warp is a worker
 // of its own with a ring of TMA tiles in shared memory (K and V of a block are 64 x d bytes
 // each), and the blocks of all (sequence, head, tile) segments, laid out one after another, are
 // cut into equal ranges, one for each worker, whatever the lengths.  A range may begin or end
