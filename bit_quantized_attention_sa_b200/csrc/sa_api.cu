@@ -942,8 +942,14 @@ sa_status sa_rope(const sa_rope_tensor *tensors, int count, int dtype, int B, in
             if (st % per16 != 0) return SA_ERR_MISALIGNED;
         // an output that is its own copy would be turned several times in place
         if ((B > 1 && t.y_batch == 0) || (t.heads > 1 && t.y_head == 0) || (N > 1 && t.y_tok == 0)) return SA_ERR_INVALID_ARG;
+        // in place means element by element: with other strides rows would be written before they are read
+        if (t.x == t.y && ((B > 1 && t.x_batch != t.y_batch) || (t.heads > 1 && t.x_head != t.y_head) ||
+                           (N > 1 && t.x_tok != t.y_tok)))
+            return SA_ERR_INVALID_ARG;
         a.io[i] = RopeIo{t.x, t.y, t.x_batch, t.x_head, t.x_tok, t.y_batch, t.y_head, t.y_tok, t.heads};
     }
+    if (count == 2 && (tensors[0].y == tensors[1].y || tensors[0].y == tensors[1].x || tensors[1].y == tensors[0].x))
+        return SA_ERR_INVALID_ARG;  // one tensor's blocks would write what the other's read or write
     if (!pos || !freqs) return SA_ERR_INVALID_ARG;
     if (!aligned(pos, 4) || !aligned(freqs, 8)) return SA_ERR_MISALIGNED;
     const sa_status r = check_device();

@@ -327,7 +327,7 @@ sa_status sa_rope_frequencies(int rot, double base, int scaling, double factor, 
 /* One tensor of a rotation: x -> y, [B, heads, N, d] by element strides of batch, head and
  * token (channels contiguous).  y == x with equal strides rotates in place; x and y must not
  * overlap in any other way, nor y's elements each other (a stride of 0 over more than one is
- * refused). */
+ * refused, and so is y == x with other strides).  Of two tensors, neither's y is the other's x or y. */
 typedef struct {
     const void *x;
     void *y;

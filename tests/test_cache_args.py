@@ -112,6 +112,27 @@ def test_rope_refuses_an_output_over_itself(libsa, kw):
     assert _rope(libsa.raw_library(), x_head=0, x_tok=0, y_head=0, y_tok=0, B=0) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(y_head=1152), dict(y_tok=256), dict(x_tok=0), dict(x_head=0), dict(B=2, y_batch=1 << 16)])
+def test_rope_refuses_in_place_with_other_strides(libsa, kw):
+    assert _rope(libsa.raw_library(), **kw) == 1
+
+
+def test_rope_refuses_tensors_that_write_each_other(libsa):
+    lib = libsa.raw_library()
+
+    def call(x0, y0, x1, y1):
+        t = (RopeTensor * 2)(*(RopeTensor(x, y, 0, 1024, 128, 0, 1024, 128, 4) for x, y in ((x0, y0), (x1, y1))))
+        # a call that passes this check is refused for its misaligned positions
+        return lib.sa_rope(t, 2, 0, 1, 8, 128, 128, 0, FAKE + 2, 0, 0, 1, None, FAKE, ctypes.c_float(1.0), 0, None)
+
+    a, b, c = FAKE, FAKE + (1 << 20), FAKE + (2 << 20)
+    assert call(a, b, c, b) == 1    # one output for both
+    assert call(a, b, b, c) == 1    # q' over k
+    assert call(a, c, b, a) == 1    # k' over q
+    assert call(a, a, b, b) == 3    # in place, each its own
+    assert call(a, b, a, c) == 3    # one input for both
+
+
 def test_binding_refusals(libsa):
     x = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
     cache = tuple(libsa.sa_cache_alloc(4, 2, 128, device="cpu"))
