@@ -569,14 +569,20 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
     __shared__ float sums[kCombineWarps][D];
     chain_begin();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int4 mine = blockIdx.x + lane * gridDim.x < workers ? A.meta[2 * (blockIdx.x + lane * gridDim.x)] : make_int4(0, 0, 0, 0);
+    // lane k looks at worker blockIdx.x + k * gridDim.x; both words come at once (the second may be old, unless used)
+    int4 mine = make_int4(0, 0, 0, 0), place = mine;
+    if (blockIdx.x + lane * gridDim.x < workers) {
+        mine = A.meta[2 * (blockIdx.x + lane * gridDim.x)];
+        place = A.meta[2 * (blockIdx.x + lane * gridDim.x) + 1];
+    }
     uint32_t found = __ballot_sync(0xffffffffu, mine.x > 0);
     while (found) {
         const int k = __ffs(found) - 1, w = blockIdx.x + k * gridDim.x;
         found &= found - 1;
         const int pieces = __shfl_sync(0xffffffffu, mine.x, k), slot0 = __shfl_sync(0xffffffffu, mine.y, k);
-        const int4 where = A.meta[2 * w + 1];  // first token, head, row of the segment in its head, its rows
-        const int row0 = where.z, rows = where.w;
+        // first token, head, row of the segment in its head, its rows
+        const int first = __shfl_sync(0xffffffffu, place.x, k), head = __shfl_sync(0xffffffffu, place.y, k);
+        const int row0 = __shfl_sync(0xffffffffu, place.z, k), rows = __shfl_sync(0xffffffffu, place.w, k);
         int groups = 1;
         while (groups < rows && groups < kCombineWarps) groups *= 2;
         const int subs = kCombineWarps / groups, sub = warp / groups;
@@ -603,17 +609,22 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
             load(sub);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) out[e] = 0.0f;
+            float own = -INFINITY;  // the lane's maximum, which its total is relative to
             if (r < rows) {
-                for (int p = lane; p < pieces; p += 32) big = fmaxf(big, part_of(p)[ROWS * D + r]);
+                for (int p = lane; p < pieces; p += 32) {
+                    const float *part = part_of(p);
+                    const float pm = part[ROWS * D + r], pl = part[ROWS * (D + 1) + r];
+                    const float next = fmaxf(own, pm), to = next == -INFINITY ? 0.0f : next;
+                    total = total * ex2_approx(own - to) + pl * ex2_approx(pm - to);
+                    own = next;
+                }
+                big = own;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             }
             const float ref = big == -INFINITY ? 0.0f : big;
             if (r < rows) {
-                for (int p = lane; p < pieces; p += 32) {
-                    const float *part = part_of(p);
-                    total += ex2_approx(part[ROWS * D + r] - ref) * part[ROWS * (D + 1) + r];
-                }
+                total *= ex2_approx(own - ref);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             }
@@ -641,7 +652,7 @@ __global__ void __launch_bounds__(kCombineThreads, 3) cache_combine_kernel(const
             if (r >= rows || sub > 0) continue;
             const float f = total == 0.0f ? 0.0f : 1.0f / total;
             const int rr = row0 + r, i = rr / A.G;
-            const int64_t at = (int64_t(where.x) + i) * (A.H * A.G) + where.y * A.G + rr - i * A.G;
+            const int64_t at = (int64_t(first) + i) * (A.H * A.G) + head * A.G + rr - i * A.G;
             uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(A.o) + at * D + lane * kPer);
 #pragma unroll
             for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_out(out[e] * f, out[e + 1] * f, T());
