@@ -892,9 +892,10 @@ sa_status sa_rope_frequencies(int rot, double base, int scaling, double factor, 
     };
     double lo = 0.0, hi = 0.0;
     if (ramp) {
-        lo = std::max(0.0, std::floor(pair_of(beta_fast)));
-        hi = std::min(rot / 2 - 1.0, std::ceil(pair_of(beta_slow)));
-        hi = std::max(hi, lo + 1e-3);  // a step, where both borders fall on one pair
+        // the borders may lie outside the pairs (a long context turns every pair more than beta_slow
+        // times): only the share is clamped
+        lo = std::floor(pair_of(beta_fast));
+        hi = std::max(std::ceil(pair_of(beta_slow)), lo + 1e-3);  // a step, where both fall on one pair
     }
     for (int i = 0; i < rot / 2; ++i) {
         const double f = std::pow(base, -2.0 * i / rot);

@@ -318,7 +318,9 @@ enum { SA_CACHE_PAGE = 64 };
  *                   slowest divided by factor;
  *   SA_ROPE_RAMP    pairs that turn more than beta_fast times within original_len positions as
  *                   they were, those that turn less than beta_slow times divided by factor, the
- *                   ones between mixed linearly in the pair's index; amplitude
+ *                   ones between mixed linearly in the pair's index, from the (real) index that
+ *                   turns beta_fast times, rounded down, to the one that turns beta_slow times,
+ *                   rounded up, both of which may lie outside the pairs; amplitude
  *                   0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023).
  * base > 1, factor >= 1; original_len >= 1 and beta_fast > beta_slow > 0 for SA_ROPE_RAMP. */
 sa_status sa_rope_frequencies(int rot, double base, int scaling, double factor, int original_len,
