@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/sa.h"
+#include "sa_cache_attn.cuh"
 #include "sa_internal.h"
 
 namespace sa {
@@ -1097,6 +1098,12 @@ size_t sa_cache_attn_workspace_bytes(int64_t T, int B, int H, int group, int d)
     if (T < 0 || B < 1 || H < 1 || (d != 64 && d != 128) || check_group(T, H, group) != SA_OK) return 0;
     const int sms = device_sms();
     return sms < 1 ? 0 : cache_attn_workspace(sms, T, B, group, d);
+}
+
+int64_t sa_debug_cache_steps(int n, int len, int group, int causal, int window)
+{
+    if (n < 0 || len < 0 || len > (1 << 30) || group < 1 || int64_t(n) * group > (1 << 30) || window < 0) return -1;
+    return steps_of(n, len, group, causal, std::min(window, 1 << 30), 0, 1);
 }
 
 sa_status sa_debug_qk_s32(const int8_t *q_i8, const int8_t *k_i8, int B, int H, int N, int d,

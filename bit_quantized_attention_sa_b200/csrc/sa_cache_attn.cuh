@@ -64,6 +64,33 @@ __device__ __forceinline__ bool load_span(const CacheAttnArgs &A, int b, int &ts
     return false;
 }
 
+// The tensor-core kernel's work: a segment is kRowsSeg rows (query token and shared head) of a
+// sequence, a step two blocks of keys.  Segment p of the n new tokens of a sequence with len cached
+// ones, G query heads on each head, sees the blocks [blo, bhi), at least one step.
+constexpr int kRowsSeg = 256;
+struct Reach {
+    int blo, bhi;
+    __host__ __device__ int steps() const { return bhi - blo > 2 ? (bhi - blo + 1) / 2 : 1; }
+};
+__host__ __device__ __forceinline__ Reach reach_of(int n, int len, int G, int causal, int window, int p)
+{
+    const int rows = n * G, pos0 = len - n, end = p * kRowsSeg + kRowsSeg;
+    const int i_lo = p * kRowsSeg / G, i_hi = ((rows < end ? rows : end) - 1) / G;
+    const int last = causal || pos0 + i_hi < 0 ? pos0 + i_hi : len - 1;
+    const int seen = pos0 + i_lo - window + 1, first = window > 0 && seen > 0 ? seen : 0;
+    Reach r;
+    r.blo = first / kPage;
+    r.bhi = last < first ? r.blo : last / kPage + 1;
+    return r;
+}
+// Steps of its segments p0, p0 + stride, ...: 2^22 segments of 2^23 steps are accepted, so 64 bits.
+__host__ __device__ __forceinline__ int64_t steps_of(int n, int len, int G, int causal, int window, int p0, int stride)
+{
+    int64_t sum = 0;
+    for (int p = p0; p < (n * G + kRowsSeg - 1) / kRowsSeg; p += stride) sum += reach_of(n, len, G, causal, window, p).steps();
+    return sum;
+}
+
 // The reference that value scales are taken relative to: the power of two at or below x > 0 (a
 // power of two, so that the rounding of a weight does not depend on the scales of blocks that
 // its row does not see).

@@ -49,7 +49,6 @@ constexpr int kWarpConvert = 8, kWarpQK = 12, kWarpPV = 13;
 constexpr int kStages = 4;  // fp16 tiles
 constexpr int kRaw = 2;     // tiles of codes on their way
 constexpr int kWindow = 16;  // steps whose scales are in shared memory, two windows in turn for each tile
-constexpr int kRowsSeg = 256;
 constexpr uint32_t kTmemCols = 512, kColS = 0;
 __host__ __device__ constexpr uint32_t col_p(int t) { return 128u + 64u * uint32_t(t); }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * uint32_t(t); }
@@ -81,21 +80,13 @@ __device__ __forceinline__ Seq load_seq(const CacheAttnArgs &A, int b)
     return s;
 }
 
-// What segment p of a sequence sees: blocks [blo, bhi), at least one step.
-struct Reach {
-    int blo, bhi;
-    __device__ int steps() const { return max(1, (bhi - blo + 1) / 2); }
-};
 __device__ __forceinline__ Reach reach_of(const CacheAttnArgs &A, const Seq &s, int p)
 {
-    const int rows = s.n * A.G, pos0 = s.len - s.n;
-    const int i_lo = p * kRowsSeg / A.G, i_hi = min(rows - 1, p * kRowsSeg + kRowsSeg - 1) / A.G;
-    const int last = A.causal || pos0 + i_hi < 0 ? pos0 + i_hi : s.len - 1;
-    const int first = A.window > 0 ? max(0, pos0 + i_lo - A.window + 1) : 0;
-    Reach r;
-    r.blo = first / kPage;
-    r.bhi = last < first ? r.blo : last / kPage + 1;
-    return r;
+    return sa::reach_of(s.n, s.len, A.G, A.causal, A.window, p);
+}
+__device__ __forceinline__ int64_t steps_of(const CacheAttnArgs &A, const Seq &s, int p0, int stride)
+{
+    return sa::steps_of(s.n, s.len, A.G, A.causal, A.window, p0, stride);
 }
 
 // The pieces of this block's range, one after another.  Each warp has its own in shared memory,
@@ -164,7 +155,7 @@ struct Sizes {
     static constexpr int kPart = kRowsSeg * (D + 2);
 };
 static_assert(Sizes<128>::kAlloc <= 227 * 1024, "shared memory per CTA");
-static_assert(4 * kCacheChunkMaxSeqs <= kStages * Sizes<64>::kTileBytes, "the costs fit the ring before it is used");
+static_assert(8 * kCacheChunkMaxSeqs <= kStages * Sizes<64>::kTileBytes, "the costs fit the ring before it is used");
 
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -339,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     int64_t *range = reinterpret_cast<int64_t *>(smem + S::kOffMisc);   // flattened start, total
     int *first = reinterpret_cast<int *>(smem + S::kOffMisc + 16);      // sequence, head, segment and step of the start
     uint32_t *tmem_word = reinterpret_cast<uint32_t *>(smem + S::kOffMisc + 32);
-    int *cost = reinterpret_cast<int *>(smem + S::kOffKv);  // steps of a sequence's segments, of one head
+    int64_t *cost = reinterpret_cast<int64_t *>(smem + S::kOffKv);  // steps of a sequence's segments, of one head
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = reinterpret_cast<int *>(smem + S::kOffMisc + 36);
@@ -376,15 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     if (A.B > 64) {
         for (int b = threadIdx.x; b < A.B; b += kThreads) {
             const Seq s = load_seq(A, b);
-            int sum = 0;
-            for (int p = 0; p < s.pairs; ++p) sum += reach_of(A, s, p).steps();
-            cost[b] = sum;
+            cost[b] = steps_of(A, s, 0, 1);
         }
     } else for (int b = warp; b < A.B; b += kThreads / 32) {
         const Seq s = load_seq(A, b);
-        int sum = 0;
-        for (int p = lane; p < s.pairs; p += 32) sum += reach_of(A, s, p).steps();
-        sum = __reduce_add_sync(0xffffffffu, sum);
+        int64_t sum = steps_of(A, s, lane, 32);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) cost[b] = sum;
     }
     tc_fence_before();
@@ -406,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
             int64_t before = 0;
             int b = 0;
             for (; b < A.B; b += 32) {  // 32 sequences at a time: those that end at or before the start
-                const int64_t mine = b + lane < A.B ? int64_t(cost[b + lane]) * A.H : 0;
+                const int64_t mine = b + lane < A.B ? cost[b + lane] * A.H : 0;
                 int64_t incl = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -423,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 before += __shfl_sync(0xffffffffu, incl, 31);
             }
             const Seq s = load_seq(A, b);
-            int rem = int((start - before) % cost[b]);
+            int64_t rem = (start - before) % cost[b];
             const int h = int((start - before) / cost[b]);
             int p = 0;
             for (; p < s.pairs; p += 32) {
@@ -447,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 first[0] = b;
                 first[1] = h;
                 first[2] = p;
-                first[3] = rem;
+                first[3] = int(rem);
             }
         }
     }

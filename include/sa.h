@@ -392,6 +392,10 @@ sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T
  * that it refuses, or no device). */
 size_t sa_cache_attn_workspace_bytes(int64_t T, int B, int H, int group, int d);
 
+/* Debug (host only): the steps of 256 rows by 128 keys that sa_cache_attn's tensor-core kernel
+ * takes for each key/value head of a sequence of n queries over len cached tokens (-1: refused). */
+int64_t sa_debug_cache_steps(int n, int len, int group, int causal, int window);
+
 /* Debug: the int32 S = q_i8 . k_i8^T tiles computed by the same tcgen05 INT8 path the
  * attention kernel uses, stored to s_out int32 [B,H,Npad,Npad] (padded rows/keys
  * included).  For bit-exact checks on small problems only.  Allocates nothing. */
