@@ -47,6 +47,8 @@ namespace {
 // 70 / 76; 24 rows, which are read twice here: 78 / 71, 252 / 237, 85 / 77.
 constexpr int kFewRows = 16;
 constexpr float kPScale = 16384.0f;
+// Blocks of one worker, two tiles each, are counted in 32 bits; a call of more (minutes of work) is left out.
+constexpr int64_t kMaxChunk = 1 << 29;
 
 // D: head size; NT: tiles of eight rows that a warp works on at once.  One tile leaves registers
 // for twelve warps, with a ring of two slots (a K or V tile of 64 x D bytes each); two tiles for
@@ -153,7 +155,11 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
     int64_t before = 0;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     prefix[threadIdx.x] = before + incl - mine;
-    if (threadIdx.x == kThreads - 1) prefix[kThreads] = before + incl;
+    if (threadIdx.x == kThreads - 1) {
+        const bool fits = before + incl <= kMaxChunk * kWarps * int64_t(gridDim.x);
+        if (!fits) record(8);
+        prefix[kThreads] = fits ? before + incl : 0;
+    }
     __syncthreads();
     const int64_t total = prefix[kThreads];
 

@@ -298,7 +298,9 @@ sa_status sa_sla_fwd(const void *q, const void *k, const void *v, void *o, int B
  *     64 * max_pages, offsets that decrease or pass T) sets SA_ERR_BAD_INDEX in the device
  *     status word: nothing is stored through it, a bad page reads as NaN, and a sequence whose
  *     length or offsets are bad is left out, its output rows as they were (appending and
- *     reading may leave out others beside offsets that decrease).
+ *     reading may leave out others beside offsets that decrease).  Attention of few rows (16 of a
+ *     sequence and head or fewer on average) leaves out, in the same way, a call of more than 2^39
+ *     blocks, counted for each head and each 8 rows.
  *   - T = 0 (N = 0) is a valid call that does nothing.
  *   - The codes, k, v, q, o, x, y and the workspace are 16-byte aligned; freqs 8-byte; the int32
  *     and the other fp32 arrays 4-byte.  Token strides are in elements, multiples of 16 bytes, and at
