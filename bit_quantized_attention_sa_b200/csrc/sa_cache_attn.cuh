@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "sa_internal.h"
+#include "sa_ptx.cuh"
 
 namespace sa {
 
@@ -98,6 +99,22 @@ __device__ __forceinline__ float scale_ref(float x)
 {
     return fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 1.17549435e-38f);
 }
+
+// log2 of a value scale: -inf for 0, NaN for one that is not finite (its block reads as NaN).
+__device__ __forceinline__ float log2_scale(float s) { return s < INFINITY ? log2f(s) : __int_as_float(0x7fffffff); }
+
+// Weights are 2^(x + log2 scale_v + bits - w) while they are summed, relative to 2^m when the sums are
+// written: f * power = 2^(w - m - bits), in two factors where one would leave the normal range (value
+// scales below about 2^-100).  The sums are 0 where w = -inf (no scale above 0).
+__device__ __forceinline__ void power_of(float w, float m, float bits, float &f, float &power)
+{
+    const float k = w == -INFINITY ? 0.0f : w - m - bits, near = fminf(fmaxf(k, -100.0f), 100.0f);
+    f = ex2_approx(k - near);
+    power = ex2_approx(near);
+}
+// A step's sum of p is taken from the weights as long as the one at x = m is 2^-90 or more, so that
+// those 2^-30 of it are still normal.
+constexpr float kAtLeast = -90.0f;
 
 // The power of two, and its inverse, that brings a row whose largest magnitude is `top` to
 // [1, 4): bf16 has more range than fp16.  Values that leave fp16's normal range then are below

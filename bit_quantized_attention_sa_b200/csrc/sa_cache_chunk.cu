@@ -22,11 +22,12 @@
 // P is the A operand from tensor memory, which halves P . V's reading of shared memory.  S has
 // one buffer for both tiles in turn, which staggers the two softmax groups by half a step.
 //
-// Rounding.  P is rounded to fp16 as 2^5 * p * scale_v / u, u a running reference of the value
-// scales (a power of two, raised when a scale exceeds 4 u) and p relative to a reference m of the row's maximum
-// (raised when the maximum exceeds m + 8, in powers of two), so it stays within 2^15 and acc is
-// rescaled rarely; relative error 2^-11, subnormals below 2^-19 of the reference.  The factor is
-// folded into the exponent, and a block's sum of p divided by it again in fp32.
+// Rounding.  P is rounded to fp16 as 2^7 * p * scale_v / 2^w: both are powers of two in the exponent,
+// x + log2 scale_v - w, and w is a whole number at most 8 below the row's largest such sum so far (raised
+// then, which rescales acc, to the next whole number), so P stays within 2^15 and acc is rescaled rarely.
+// Relative error 2^-11; products below 2^-20 of the row's largest are fp16 subnormals.  w is the row's
+// own, over the keys that it sees: no block that it does not see, and no other row, changes it.  The sum of
+// p is relative to 2^m, m the maximum rounded up: a block's sum of P's exponentials times one power.
 //
 // Work.  The steps of all segments, laid out one after another (sequence, head, rows), are cut
 // into equal ranges, one for each SM, as in sa_cache_attn.cu; pieces of segments that two or more
@@ -55,7 +56,7 @@ __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * uint3
 constexpr uint32_t kRegsSoftmax = 176, kRegsConvert = 88, kRegsIssue = 72, kLaunchRegs = 128;
 static_assert(128 * (2 * kRegsSoftmax + kRegsConvert + kRegsIssue) <= kLaunchRegs * kThreads,
               "the register split must fit the registers the block is launched with");
-constexpr float kGrow = 8.0f;
+constexpr float kGrow = 8.0f, kPBits = 7.0f;  // see Rounding above
 constexpr uint32_t kMinusInf = 0xff800000u;
 
 constexpr int kBarQFull = 0, kBarKvFull = 2, kBarKvEmpty = kBarKvFull + kStages, kBarSFull = kBarKvEmpty + kStages,
@@ -305,18 +306,22 @@ __device__ __forceinline__ void p32(const uint32_t (&s)[32], uint64_t c, uint64_
         }
     }
 }
-// The same for any mask (unseen keys have the score -inf) and scales, p apart from its factor f:
-// what is not seen is 0 whatever the scales.
-__device__ __forceinline__ void p32_any(const uint32_t (&s)[32], float c, float bias, float f, float (&sum)[4], uint32_t (&pw)[16])
+// The same for any mask (unseen keys have the score -inf) and scales: what is not seen is 0 whatever
+// the scales.  A row whose sum can be taken from its weights gets the very sums of p32, so that it does
+// not depend on the rows that brought its warp here; the others' are those of 2^(s * c - m).
+__device__ __forceinline__ void p32_any(const uint32_t (&s)[32], float c, float bias, bool apart, float m, float (&sum)[4],
+                                        uint32_t (&pw)[16])
 {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        const bool k0 = s[i] != kMinusInf, k1 = s[i + 1] != kMinusInf;
-        const float e0 = k0 ? ex2_approx(fmaf(fl_of(s[i]), c, bias)) : 0.0f;
-        const float e1 = k1 ? ex2_approx(fmaf(fl_of(s[i + 1]), c, bias)) : 0.0f;
-        sum[0] += e0;
-        sum[1] += e1;
-        pw[i / 2] = pack_h2(k0 ? e0 * f : 0.0f, k1 ? e1 * f : 0.0f);
+        float p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool seen = s[i + k] != kMinusInf;
+            p[k] = seen ? ex2_approx(fmaf(fl_of(s[i + k]), c, bias)) : 0.0f;
+            sum[(i & 2) + k] += !apart ? p[k] : seen ? ex2_approx(fmaf(fl_of(s[i + k]), c, -m)) : 0.0f;
+        }
+        pw[i / 2] = pack_h2(p[0], p[1]);
     }
 }
 
@@ -689,44 +694,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarQFull + t));
             }
-            float m = -INFINITY, l = 0.0f, u = 0.0f;
-            // The scales go to shared memory, for each block scale_k and f = 2^5 scale_v / u.  The four warps
+            float m = -INFINITY, l = 0.0f, w_ref = -INFINITY;
+            // The scales go to shared memory, for each block scale_k and log2 scale_v.  The four warps
             // of the tile write the same values, two windows in turn: none is further than into its next
             // window while another reads the one before, for each S needs all four to have read the last.
             uint32_t scales = 0;
             for (int j = 0; j < w.count; ++j, ++c) {
-                float su = 1.0f;
                 if (j % kWindow == 0) {
                     scales = sbase + S::kOffScale + uint32_t(2 * t + (turn++ & 1)) * (2 * kWindow * 8);
                     const int blk = w.r.blo + 2 * (w.off + j) + lane;
-                    // the reference of the value scales; one that is not finite leaves it
-                    const float top = __uint_as_float(
-                        __reduce_max_sync(0xffffffffu, sv_n > 0.0f && sv_n < INFINITY ? __float_as_uint(sv_n) : 0u));
-                    if (top > 4.0f * u) {
-                        const float u_new = scale_ref(top);
-                        su = u / u_new;
-                        u = u_new;
-                    }
                     if (blk < w.r.bhi)
-                        st_shared_f2(scales + 8 * lane, sk_n, sv_n == 0.0f ? 0.0f : 32.0f * (sv_n / u));
+                        st_shared_f2(scales + 8 * lane, sk_n, log2_scale(sv_n));
                     else
-                        st_shared_f2(scales + 8 * lane, 1.0f, 32.0f);  // no such block: none of its keys is seen
+                        st_shared_f2(scales + 8 * lane, 1.0f, 0.0f);  // no such block: none of its keys is seen
                     __syncwarp();
                     scales_at(j + kWindow, page_n, sk_n, sv_n);
                     page_n = page_at(j + 2 * kWindow);
                 }
-                float c0, c1;
-                bool plain, edge;
                 const int t0 = (w.r.blo + 2 * (w.off + j)) * kPage;
-                {
-                    const float4 b = ld_shared_f4(scales + 16 * (j % kWindow));  // of both blocks
-                    c0 = rc * b.x;
-                    c1 = rc * b.z;
-                    // else f is applied apart from the exponent, and unseen keys need more than a score of -inf
-                    plain = __all_sync(0xffffffffu, b.y > 1e-15f && b.y < INFINITY && b.w > 1e-15f && b.w < INFINITY &&
-                                                        c0 > 0.0f && c0 < INFINITY && c1 > 0.0f && c1 < INFINITY);
-                    edge = __any_sync(0xffffffffu, lo > t0 || hi < t0 + 2 * kPage);
-                }
+                const bool edge = __any_sync(0xffffffffu, lo > t0 || hi < t0 + 2 * kPage);
+                const float4 b = ld_shared_f4(scales + 16 * (j % kWindow));  // of both blocks
+                const float c0 = rc * b.x, c1 = rc * b.z;
                 if (!wait(kBarSFull + t, c)) break;
                 uint32_t s[4][32];
                 tc_fence_after();
@@ -747,44 +735,55 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 }
                 // the scales are not negative, so they commute with the maximum (0 * -inf is
                 // a NaN, which fmaxf passes over)
-                const float top = fmaxf(max64(s[0], s[1]) * c0, max64(s[2], s[3]) * c1);
+                const float top0 = max64(s[0], s[1]) * c0, top1 = max64(s[2], s[3]) * c1;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarSEmpty));
 
-                float f = su;  // what acc is rescaled by
-                if (top > m + kGrow || (m == -INFINITY && top > m)) {
-                    const float alpha = ex2_approx(m - top);
-                    f *= alpha;
-                    l *= alpha;
-                    m = top;
+                const float top = fmaxf(top0, top1), most = fmaxf(top0 + b.y, top1 + b.w);
+                float f = 1.0f;  // what acc is rescaled by
+                if (top > m) {
+                    const float up = ceilf(top);
+                    l *= ex2_approx(m - up);
+                    m = up;
                 }
+                if (most > w_ref + kGrow || (w_ref == -INFINITY && most > w_ref)) {
+                    const float up = ceilf(most);
+                    f = ex2_approx(w_ref - up);
+                    w_ref = up;
+                }
+                // bias: P = 2^(x + bias); at: the exponent of P at x = m
+                const float ref = m == -INFINITY ? 0.0f : m, base = kPBits - (w_ref == -INFINITY ? 0.0f : w_ref);
+                const float bias0 = base + b.y, bias1 = base + b.w, at0 = bias0 + ref, at1 = bias1 + ref;
+                // else P may vanish where p does not, and unseen keys need more than a score of -inf
+                const bool plain0 = at0 >= kAtLeast && c0 > 0.0f && c0 < INFINITY;
+                const bool plain1 = at1 >= kAtLeast && c1 > 0.0f && c1 < INFINITY;
+                const bool plain = __all_sync(0xffffffffu, plain0 && plain1);
                 // P's columns and acc are free once P . V of the step before is done
                 if (c >= 1 && !wait(kBarPvDone + t, c - 1)) break;
                 tc_fence_after();
-                const float ref = m == -INFINITY ? 0.0f : m;
-                const float4 b = ld_shared_f4(scales + 16 * (j % kWindow));
                 if (plain) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t pw[16];
                         uint64_t sum[2] = {0, 0};
-                        const float cc = k < 2 ? c0 : c1, f = k < 2 ? b.y : b.w, bias = __log2f(f) - ref;
+                        const float cc = k < 2 ? c0 : c1, bias = k < 2 ? bias0 : bias1;
                         p32(s[k], pair(cc, cc), pair(bias, bias), sum, pw);
                         tmem_st16(tmem + lane_addr + col_p(t) + 16 * k, pw);
                         float x0, x1, x2, x3;
                         unpair(x0, x1, sum[0]);
                         unpair(x2, x3, sum[1]);
-                        l = fmaf((x0 + x1) + (x2 + x3), __frcp_rn(f), l);
+                        l = fmaf((x0 + x1) + (x2 + x3), ex2_approx(k < 2 ? -at0 : -at1), l);
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t pw[16];
                         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        p32_any(s[k], k < 2 ? c0 : c1, -ref, k < 2 ? b.y : b.w, sum, pw);
+                        const bool apart = !(k < 2 ? plain0 : plain1);
+                        p32_any(s[k], k < 2 ? c0 : c1, k < 2 ? bias0 : bias1, apart, ref, sum, pw);
                         tmem_st16(tmem + lane_addr + col_p(t) + 16 * k, pw);
-                        l += sum[0] + sum[1];
+                        l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), apart ? 1.0f : ex2_approx(k < 2 ? -at0 : -at1), l);
                     }
                 }
                 if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
@@ -816,7 +815,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 const int64_t at = (int64_t(w.s.ts) + i) * (A.H * A.G) + w.h * A.G + rr - i * A.G;
                 const bool whole = w.begins && w.ends;
                 const int slot = 2 * wk + (w.pieces == 0 ? 0 : 1);
-                const float f = whole ? (l == 0.0f ? 0.0f : u / (32.0f * l)) : u * 0.03125f;
+                float f, power;
+                power_of(w_ref, m, kPBits, f, power);
+                if (whole) f = l == 0.0f ? 0.0f : f / l;
                 float *part = A.part + int64_t(slot) * S::kPart;
                 if (w.begins && !w.ends) {
                     split = true;
@@ -835,21 +836,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                     uint32_t r[32];
                     tmem_ld32_wait(tmem + lane_addr + col_o(t) + 32 * k, r);
                     if (!valid) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(fl_of(r[e]) * f * power);
                     if (whole) {
                         T *dst = static_cast<T *>(A.o) + at * D + 32 * k;
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             *reinterpret_cast<uint4 *>(dst + e) =
-                                make_uint4(pack_out(fl_of(r[e]) * f, fl_of(r[e + 1]) * f, T()),
-                                           pack_out(fl_of(r[e + 2]) * f, fl_of(r[e + 3]) * f, T()),
-                                           pack_out(fl_of(r[e + 4]) * f, fl_of(r[e + 5]) * f, T()),
-                                           pack_out(fl_of(r[e + 6]) * f, fl_of(r[e + 7]) * f, T()));
+                                make_uint4(pack_out(fl_of(r[e]), fl_of(r[e + 1]), T()),
+                                           pack_out(fl_of(r[e + 2]), fl_of(r[e + 3]), T()),
+                                           pack_out(fl_of(r[e + 4]), fl_of(r[e + 5]), T()),
+                                           pack_out(fl_of(r[e + 6]), fl_of(r[e + 7]), T()));
                     } else {
                         float *dst = part + (8 * k * kRowsSeg + t * 128 + row) * 4;  // [D / 4][row][4]
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(dst + e * kRowsSeg) = make_float4(fl_of(r[e]) * f, fl_of(r[e + 1]) * f,
-                                                                               fl_of(r[e + 2]) * f, fl_of(r[e + 3]) * f);
+                            *reinterpret_cast<float4 *>(dst + e * kRowsSeg) =
+                                make_float4(fl_of(r[e]), fl_of(r[e + 1]), fl_of(r[e + 2]), fl_of(r[e + 3]));
                     }
                 }
             }
