@@ -8,10 +8,13 @@
 // with m, l and acc in fp32; in the end o = acc / l and lse = m + log l.
 //
 // The codes are exact in fp16, and so is q after a power of two for each row (its exponent goes
-// into the row's score scale), so S has no rounding before its fp32 accumulator.  p times the
-// ratio of scale_v[j] to u, the power of two below the largest scale_v so far, is rounded to
-// fp16, 2^14 times itself: at most 2^15, relative error 2^-11, and what is below 2^-28 of the
-// row's largest weight falls to fp16's subnormals.  acc is kept in units of u * 2^-14.
+// into the row's score scale), so S has no rounding before its fp32 accumulator.  P, rounded to
+// fp16, is 2^15 * p * scale_v[j] / 2^w, both powers of two in the exponent (in powers of two,
+// x + log2 scale_v[j] - w): w, a whole number, is the row's largest such sum so far, rounded up.  So P
+// is at most 2^15, its relative error 2^-11, and what is below 2^-29 of the row's largest product of
+// weight and scale falls to fp16's subnormals.  w is over the keys that the row sees: no block that it
+// does not see, and no other row of the tile, changes it.  acc is kept in units of 2^(w - 15); the sum of
+// p, relative to 2^m with m rounded up, is the sum of P before its rounding times a power of two.
 //
 // What bounds it: reading 2 d bytes for each cached token and head.  Measured, 4 sequences of
 // 70001 to 131072 tokens, 32 query heads on 8 of 128: 154 us for 900 MB, 5.9 TB/s (a plain copy
@@ -46,7 +49,7 @@ namespace {
 // one, us): 16 rows, 16 sequences of 4000 tokens 50 / 70, 64 of them 140 / 234, one of 60000
 // 70 / 76; 24 rows, which are read twice here: 78 / 71, 252 / 237, 85 / 77.
 constexpr int kFewRows = 16;
-constexpr float kPScale = 16384.0f;
+constexpr float kPBits = 15.0f;
 // Blocks of one worker, two tiles each, are counted in 32 bits; a call of more (minutes of work) is left out.
 constexpr int64_t kMaxChunk = 1 << 29;
 
@@ -106,7 +109,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 struct Entry {
     int b, seg, blk;   // sequence, head * tiles + tile, block of the sequence (absolute)
     int line;          // first 128-byte line of its tiles in the cache
-    float sk, sv;
+    float sk, lg;      // scale_k and log2 scale_v
 };
 
 template <typename T, int D, int NT>
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         e.seg = 0;
         e.blk = 0;
         e.line = 0;
-        e.sk = e.sv = 0.0f;
+        e.sk = e.lg = 0.0f;
         if (cb >= A.B) return e;
         const uint64_t rem = uint64_t(f - cbase);
         e.seg = int(rem / uint32_t(cs.nb));
@@ -205,11 +208,11 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
             const int page = A.table[int64_t(cb) * A.max_pages + e.blk], head = e.seg / cs.tiles;
             if (page < 0 || page >= A.num_pages) {
                 record(8);
-                e.sk = e.sv = __int_as_float(0x7fffffff);
+                e.sk = e.lg = __int_as_float(0x7fffffff);
             } else {
                 e.line = (page * A.H + head) * int(S::kTile / 128);
                 e.sk = A.k_scale[int64_t(page) * A.H + head];
-                e.sv = A.v_scale[int64_t(page) * A.H + head];
+                e.lg = log2_scale(A.v_scale[int64_t(page) * A.H + head]);
             }
         }
         return e;
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
     Seq sq{};
     int head = 0, row0 = 0, tile_first = 0, tile_last = -1, all_first = 0, all_last = -1;
     uint32_t qf[NT][kSteps][2];
-    float row_c[NT][2], m[NT][2], l[NT][2], acc[NT][kMT][4], u_ref = 0.0f;
+    float row_c[NT][2], m[NT][2], w_ref[NT][2], l[NT][2], acc[NT][kMT][4];
     int row_first[NT][2], row_last[NT][2];
 
     auto arrived = [&]() -> const uint8_t * {
@@ -308,13 +311,12 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
                 const int rs = row0 + 8 * n + 2 * c + e, is = rs / A.G;
                 row_first[n][e] = first_of(is);
                 row_last[n][e] = rs < rows ? last_of(is) : -1;
-                m[n][e] = -INFINITY;
+                m[n][e] = w_ref[n][e] = -INFINITY;
                 l[n][e] = 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < kMT; ++k) acc[n][k][0] = acc[n][k][1] = acc[n][k][2] = acc[n][k][3] = 0.0f;
         }
-        u_ref = 0.0f;
     };
 
     // Writes the open segment's piece.
@@ -342,8 +344,11 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
                 for (int o = 4; o < 32; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 const int rt = 8 * n + 2 * c + e;
                 if (rt >= rows) continue;
+                float f, power;
+                power_of(w_ref[n][e], m[n][e], kPBits, f, power);
+                if (whole) f = sum == 0.0f ? 0.0f : f / sum;
+                auto out = [&](int k, int i) { return acc[n][k][i] * f * power; };
                 if (whole) {
-                    const float f = sum == 0.0f ? 0.0f : u_ref / (kPScale * sum);
                     const int rr = row0 + rt, i = rr / A.G, hq = head * A.G + rr - i * A.G;
                     const int64_t at = (int64_t(sq.ts) + i) * (A.H * A.G) + hq;
                     T *dst = static_cast<T *>(A.o) + at * D + ch;
@@ -351,21 +356,18 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kMT; k += 4)
                         *reinterpret_cast<uint4 *>(dst + 2 * k) =
-                            make_uint4(pack_out(acc[n][k][e] * f, acc[n][k][2 + e] * f, T()),
-                                       pack_out(acc[n][k + 1][e] * f, acc[n][k + 1][2 + e] * f, T()),
-                                       pack_out(acc[n][k + 2][e] * f, acc[n][k + 2][2 + e] * f, T()),
-                                       pack_out(acc[n][k + 3][e] * f, acc[n][k + 3][2 + e] * f, T()));
+                            make_uint4(pack_out(out(k, e), out(k, 2 + e), T()), pack_out(out(k + 1, e), out(k + 1, 2 + e), T()),
+                                       pack_out(out(k + 2, e), out(k + 2, 2 + e), T()), pack_out(out(k + 3, e), out(k + 3, 2 + e), T()));
                 } else {
                     float *part = A.part + int64_t(slot) * S::kPart;
                     if (g == 0) {
                         part[kRows * D + rt] = m[n][e];
                         part[kRows * (D + 1) + rt] = sum;
                     }
-                    const float f = u_ref * (1.0f / kPScale);
 #pragma unroll
                     for (int k = 0; k < kMT; k += 2)
                         *reinterpret_cast<float4 *>(part + rt * D + ch + 2 * k) =
-                            make_float4(acc[n][k][e] * f, acc[n][k][2 + e] * f, acc[n][k + 1][e] * f, acc[n][k + 1][2 + e] * f);
+                            make_float4(out(k, e), out(k, 2 + e), out(k + 1, e), out(k + 1, 2 + e));
                 }
             }
     };
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         const int at = i - window;
         const int b = __shfl_sync(0xffffffffu, cur.b, at), sg = __shfl_sync(0xffffffffu, cur.seg, at);
         const int blk = __shfl_sync(0xffffffffu, cur.blk, at);
-        const float sk = __shfl_sync(0xffffffffu, cur.sk, at), sv = __shfl_sync(0xffffffffu, cur.sv, at);
+        const float sk = __shfl_sync(0xffffffffu, cur.sk, at), lg = __shfl_sync(0xffffffffu, cur.lg, at);
         if (b != seg_b || sg != seg) {
             if (seg_b >= 0) close_segment();
             open_segment(b, sg);
@@ -427,19 +429,12 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         issue(done + kSlots, window);
         ++done;
 
-        // ---- p = exp(x - m), in powers of two; pf: P as the second operand, 8 keys by 8 rows each
+        // ---- P = 2^(x + bias); pf: as the second operand, 8 keys by 8 rows each
         uint32_t pf[NT][8];
         if (seen) {
-            float ratio, su = 1.0f;
-            if (sv >= 2.0f * u_ref && sv > 0.0f && sv < INFINITY) {
-                const float u_new = scale_ref(sv);
-                su = u_ref / u_new;
-                u_ref = u_new;
-            }
-            ratio = sv == 0.0f ? 0.0f : kPScale * (sv / u_ref);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float factor[2], ref[2], top[2] = {-INFINITY, -INFINITY};
+                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -453,15 +448,39 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
                         top[e & 1] = fmaxf(top[e & 1], x);
                     }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int o = 4; o < 32; o *= 2) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
-                    const float m_new = fmaxf(m[n][e], top[e]);
-                    ref[e] = m_new == -INFINITY ? 0.0f : m_new;
-                    const float alpha = ex2_approx(m[n][e] - ref[e]);
-                    l[n][e] *= alpha;
-                    m[n][e] = m_new;
-                    factor[e] = alpha * su;
+                if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1] || top[0] + lg > w_ref[n][0] ||
+                                                top[1] + lg > w_ref[n][1])) {
+                    float factor[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // a NaN is passed over, and -inf less 0 is left where nothing was seen yet
+                        const float m_new = fmaxf(m[n][e], ceilf(top[e])), w_new = fmaxf(w_ref[n][e], ceilf(top[e] + lg));
+                        l[n][e] *= ex2_approx(m[n][e] - (m_new == -INFINITY ? 0.0f : m_new));
+                        factor[e] = ex2_approx(w_ref[n][e] - (w_new == -INFINITY ? 0.0f : w_new));
+                        m[n][e] = m_new;
+                        w_ref[n][e] = w_new;
+                    }
+                    if (__any_sync(0xffffffffu, factor[0] != 1.0f || factor[1] != 1.0f)) {
+#pragma unroll
+                        for (int k = 0; k < kMT; ++k) {
+                            acc[n][k][0] *= factor[0];
+                            acc[n][k][1] *= factor[1];
+                            acc[n][k][2] *= factor[0];
+                            acc[n][k][3] *= factor[1];
+                        }
+                    }
+                }
+                // at: the exponent of P at x = m
+                float bias[2], at[2], sum[2] = {0.0f, 0.0f};
+                bool apart[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    bias[e] = kPBits - (w_ref[n][e] == -INFINITY ? 0.0f : w_ref[n][e]) + lg;
+                    at[e] = bias[e] + (m[n][e] == -INFINITY ? 0.0f : m[n][e]);
+                    apart[e] = !(at[e] >= kAtLeast);
                 }
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)
@@ -470,22 +489,27 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
                         float z[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float x = s[n][mt][2 * y + e], p = ex2_approx(x - ref[e]);
-                            l[n][e] += p;
-                            z[e] = p * ratio;
+                            const float x = s[n][mt][2 * y + e];
+                            z[e] = ex2_approx(x + bias[e]);
                             if (!full && x == -INFINITY) z[e] = 0.0f;  // whatever the block's scale
+                            sum[e] += z[e];
                         }
                         pf[n][2 * mt + y] = transpose8x8(h2(__floats2half2_rn(z[0], z[1])));
                     }
-                if (__any_sync(0xffffffffu, factor[0] != 1.0f || factor[1] != 1.0f)) {
+                if (__any_sync(0xffffffffu, apart[0] || apart[1])) {  // P may vanish where p does not: such rows sum p
 #pragma unroll
-                    for (int k = 0; k < kMT; ++k) {
-                        acc[n][k][0] *= factor[0];
-                        acc[n][k][1] *= factor[1];
-                        acc[n][k][2] *= factor[0];
-                        acc[n][k][3] *= factor[1];
+                    for (int e = 0; e < 2; ++e) {
+                        if (!apart[e]) continue;
+                        at[e] = sum[e] = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float x = s[n][i >> 1][2 * (i & 1) + e];
+                            sum[e] += ex2_approx(x - (m[n][e] == -INFINITY ? 0.0f : m[n][e]));
+                        }
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) l[n][e] = fmaf(sum[e], ex2_approx(-at[e]), l[n][e]);
             }
         }
 

@@ -92,14 +92,6 @@ __host__ __device__ __forceinline__ int64_t steps_of(int n, int len, int G, int 
     return sum;
 }
 
-// The reference that value scales are taken relative to: the power of two at or below x > 0 (a
-// power of two, so that the rounding of a weight does not depend on the scales of blocks that
-// its row does not see).
-__device__ __forceinline__ float scale_ref(float x)
-{
-    return fmaxf(__uint_as_float(__float_as_uint(x) & 0x7f800000u), 1.17549435e-38f);
-}
-
 // log2 of a value scale: -inf for 0, NaN for one that is not finite (its block reads as NaN).
 __device__ __forceinline__ float log2_scale(float s) { return s < INFINITY ? log2f(s) : __int_as_float(0x7fffffff); }
 

@@ -10,8 +10,10 @@ from _cache_ref import random_cache, random_table, starts_of
 
 pytestmark = pytest.mark.gpu
 
-# new tokens, cached ones, query heads on each of the key/value heads: segments of the tensor-core kernel
+# new tokens, cached ones, query heads on each of the key/value heads: segments of the tensor-core
+# kernel, and tiles of one and two times eight rows of the other one
 MANY = [(300, 1000, 1), (1000, 1000, 2), (150, 700, 5)]
+FEW = [(8, 196, 1), (16, 330, 1), (5, 1026, 3), (4, 66, 2)]
 
 
 def _case(seed, n, length, G, d, dtype=torch.bfloat16, H=2, q_scale=1.0):
@@ -30,8 +32,10 @@ def _sees_block(n, length, blk, causal, window):
     return (first < 64 * blk + 64) & (last >= 64 * blk)
 
 
-@pytest.mark.parametrize("n,length,G", MANY)
-@pytest.mark.parametrize("causal,window", [(True, 0), (True, 100), (False, 100), (True, 64)])
+@pytest.mark.parametrize("n,length,G,causal,window", [
+    (*shape, *mask) for shape in MANY for mask in [(True, 0), (True, 100), (False, 100), (True, 64)]] + [
+    (*shape, True, 0) for shape in FEW] + [
+    (*shape, causal, window) for causal in (True, False) for shape, window in zip(FEW, (64, 70, 192))])
 @pytest.mark.parametrize("power", [20, 32, 60])
 def test_blocks_that_a_row_does_not_see(libsa, cuda_ok, n, length, G, causal, window, power):
     """A block of 2^power times the others' value scale: rows that do not see it are the same, bit for
@@ -51,10 +55,10 @@ def test_blocks_that_a_row_does_not_see(libsa, cuda_ok, n, length, G, causal, wi
         assert torch.equal(got[0][~sees], clean[0][~sees]), f"block {blk}"
         assert torch.equal(got[1][~sees], clean[1][~sees]), f"block {blk}"
         strict.check(got, strict.attn_ref((*cache[:3], vs), q, starts, lens, table, causal, window), q.dtype)
-    assert tried > 1 and libsa.sa_get_device_status() == 0
+    assert tried > (n * G > 16) and libsa.sa_get_device_status() == 0
 
 
-@pytest.mark.parametrize("n,length,G", MANY)
+@pytest.mark.parametrize("n,length,G", MANY + FEW)
 @pytest.mark.parametrize("weight", [-20, -32, -44, -100])
 def test_a_large_block_of_little_weight(libsa, cuda_ok, n, length, G, weight):
     """A block of 2^32 times the value scale whose keys have about 2^weight of a row's weight: it
@@ -63,7 +67,7 @@ def test_a_large_block_of_little_weight(libsa, cuda_ok, n, length, G, weight):
     cache, q, starts, lens, table = _case(7, n, length, G, d)
     q[:] = 1.0
     cache[1] *= 0.02  # the other scores are about 0
-    page = table[0, 3].long()
+    page = table[0, length // 64 // 2].long()
     cache[0][page] = -127
     cache[1][page] = -weight * math.log(2.0) / (127 * math.sqrt(d))
     cache[3][page] *= 2.0 ** 32
@@ -71,7 +75,7 @@ def test_a_large_block_of_little_weight(libsa, cuda_ok, n, length, G, weight):
     strict.check(got, strict.attn_ref(cache, q, starts, lens, table), q.dtype)
 
 
-@pytest.mark.parametrize("n,length,G", MANY)
+@pytest.mark.parametrize("n,length,G", MANY + FEW)
 @pytest.mark.parametrize("causal,window", [(True, 0), (True, 150), (False, 0), (False, 70)])
 @pytest.mark.parametrize("spread", [8, 40, 90])
 def test_scales_of_all_sizes(libsa, cuda_ok, n, length, G, causal, window, spread):
@@ -86,7 +90,7 @@ def test_scales_of_all_sizes(libsa, cuda_ok, n, length, G, causal, window, sprea
         strict.check(got, strict.attn_ref(cache, q, starts, lens, table, causal, window), q.dtype)
 
 
-@pytest.mark.parametrize("n,length,G", MANY)
+@pytest.mark.parametrize("n,length,G", MANY + FEW)
 @pytest.mark.parametrize("power", [-112, -60, 60, 112])
 def test_scales_all_small_or_large(libsa, cuda_ok, n, length, G, power):
     cache, q, starts, lens, table = _case(11, n, length, G, 64)
