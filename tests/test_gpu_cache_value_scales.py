@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import _cache_strict as strict
-from _cache_ref import random_cache, random_table, starts_of
+from _cache_ref import random_table, starts_of
 
 pytestmark = pytest.mark.gpu
 
@@ -16,12 +16,26 @@ MANY = [(300, 1000, 1), (1000, 1000, 2), (150, 700, 5)]
 FEW = [(8, 196, 1), (16, 330, 1), (5, 1026, 3), (4, 66, 2)]
 
 
-def _case(seed, n, length, G, d, dtype=torch.bfloat16, H=2, q_scale=1.0):
-    gen = torch.Generator().manual_seed(seed)
-    pages = -(-length // 64) + 3
-    cache, table = random_cache(gen, pages, H, d), random_table(gen, [length], pages)
-    q = (q_scale * torch.randn(n, H * G, d, generator=gen)).cuda().to(dtype)
-    return list(cache), q, starts_of([n]), torch.tensor([length], dtype=torch.int32, device="cuda"), table
+def _case(seed, n, length, G, d, dtype=torch.bfloat16, q_scale=1.0):
+    """One sequence of two heads; of few rows so many of sixteen that each warp of the GPU has several
+    blocks of a sequence, one after another."""
+    blocks = -(-length // 64)
+    B, H = (8000 // (16 * blocks), 16) if (n, length, G) in FEW else (1, 2)
+    gen = torch.Generator("cuda").manual_seed(seed)
+    pages = B * blocks + 3
+    codes = [torch.randint(-127, 128, (pages, H, 64, d), generator=gen, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scale = [torch.rand((pages, H), generator=gen, device="cuda") * 0.04 + 0.005 for _ in range(2)]
+    table = random_table(torch.Generator().manual_seed(seed), [length] * B, pages)
+    q = (q_scale * torch.randn(B * n, H * G, d, generator=gen, device="cuda")).to(dtype)
+    return ([codes[0], scale[0], codes[1], scale[1]], q, starts_of([n] * B),
+            torch.tensor([length] * B, dtype=torch.int32, device="cuda"), table)
+
+
+def _check(got, cache, q, starts, lens, table, causal=True, window=0):
+    """Against 64 bits, the first three sequences."""
+    rows = starts[:4][-1].item()
+    want = strict.attn_ref(cache, q[:rows], starts[:4], lens[:3], table[:3], causal, window)
+    strict.check(tuple(t[:rows] for t in got), want, q.dtype)
 
 
 def _sees_block(n, length, blk, causal, window):
@@ -45,16 +59,16 @@ def test_blocks_that_a_row_does_not_see(libsa, cuda_ok, n, length, G, causal, wi
     clean = libsa.sa_cache_attn(cache, q, starts, lens, table, **kw)
     tried = 0
     for blk in range(-(-length // 64)):
-        sees = _sees_block(n, length, blk, causal, window)
+        sees = _sees_block(n, length, blk, causal, window).repeat(lens.shape[0])
         if sees.all() or not sees.any():
             continue
         tried += 1
         vs = cache[3].clone()
-        vs[table[0, blk].long()] *= 2.0 ** power
+        vs[table[:, blk].long()] *= 2.0 ** power
         got = libsa.sa_cache_attn((*cache[:3], vs), q, starts, lens, table, **kw)
         assert torch.equal(got[0][~sees], clean[0][~sees]), f"block {blk}"
         assert torch.equal(got[1][~sees], clean[1][~sees]), f"block {blk}"
-        strict.check(got, strict.attn_ref((*cache[:3], vs), q, starts, lens, table, causal, window), q.dtype)
+        _check(got, (*cache[:3], vs), q, starts, lens, table, causal, window)
     assert tried > (n * G > 16) and libsa.sa_get_device_status() == 0
 
 
@@ -67,12 +81,12 @@ def test_a_large_block_of_little_weight(libsa, cuda_ok, n, length, G, weight):
     cache, q, starts, lens, table = _case(7, n, length, G, d)
     q[:] = 1.0
     cache[1] *= 0.02  # the other scores are about 0
-    page = table[0, length // 64 // 2].long()
+    page = table[:, length // 64 // 2].long()
     cache[0][page] = -127
     cache[1][page] = -weight * math.log(2.0) / (127 * math.sqrt(d))
     cache[3][page] *= 2.0 ** 32
     got = libsa.sa_cache_attn(cache, q, starts, lens, table, return_lse=True)
-    strict.check(got, strict.attn_ref(cache, q, starts, lens, table), q.dtype)
+    _check(got, cache, q, starts, lens, table)
 
 
 @pytest.mark.parametrize("n,length,G", MANY + FEW)
@@ -83,11 +97,11 @@ def test_scales_of_all_sizes(libsa, cuda_ok, n, length, G, causal, window, sprea
     sharp and with flat scores."""
     for q_scale in (0.3, 6.0):
         cache, q, starts, lens, table = _case(spread + n, n, length, G, 128, q_scale=q_scale)
-        gen = torch.Generator().manual_seed(spread)
-        cache[3] *= torch.pow(2.0, (torch.rand(cache[3].shape, generator=gen) - 0.5) * spread).cuda()
+        gen = torch.Generator("cuda").manual_seed(spread)
+        cache[3] *= torch.pow(2.0, (torch.rand(cache[3].shape, generator=gen, device="cuda") - 0.5) * spread)
         cache[3][::7] = 0.0
         got = libsa.sa_cache_attn(cache, q, starts, lens, table, causal=causal, window=window, return_lse=True)
-        strict.check(got, strict.attn_ref(cache, q, starts, lens, table, causal, window), q.dtype)
+        _check(got, cache, q, starts, lens, table, causal, window)
 
 
 @pytest.mark.parametrize("n,length,G", MANY + FEW)
@@ -96,4 +110,4 @@ def test_scales_all_small_or_large(libsa, cuda_ok, n, length, G, power):
     cache, q, starts, lens, table = _case(11, n, length, G, 64)
     cache[3] *= 2.0 ** power
     got = libsa.sa_cache_attn(cache, q, starts, lens, table, return_lse=True)
-    strict.check(got, strict.attn_ref(cache, q, starts, lens, table), q.dtype)
+    _check(got, cache, q, starts, lens, table)
