@@ -44,11 +44,13 @@ def attn_ref(cache, q, starts, lens, table, causal=True, window=0, sm_scale=None
             l = w.sum(-1)
             ok = ~(l == 0)
             den = torch.where(ok, l, 1.0)
-            vz = torch.where(sees.any(0)[:, None], v, 0.0)
+            bad = torch.isnan(v).any(1)                                   # reaches the rows that see it
+            vz = torch.where((sees.any(0) & ~bad)[:, None], v, 0.0)
             o[rows, cols] = torch.einsum("ngt,td->ngd", w, vz) / den[..., None]
+            o[rows, cols] = torch.where((sees & bad).any(1)[:, None, None], math.nan, o[rows, cols])
             spread[rows, cols] = torch.einsum("ngt,td->ngd", w, vz.abs()) / den[..., None]
             lse[rows, cols] = torch.where(ok, torch.log(den) + m[..., 0], -math.inf)
-            svz = torch.where(sees.any(0), vs[page, h], 0.0)
+            svz = torch.where(sees.any(0) & ~bad, vs[page, h], 0.0)
             most[rows, cols] = (w * svz).amax(-1) / den
             reach[rows, cols] = torch.where(sees[:, None], torch.einsum("ngd,td->ngt", qq.abs(), k.abs()), 0.0).amax(-1) * scale
             log = torch.where(svz > 0, torch.log2(svz.clamp(min=1e-300)), 0.0).abs()
