@@ -61,6 +61,8 @@ _lib.sa_cache_attn.argtypes = [_P, _P, _P, _I, _L, _L, _P, _P, _P, _I, _I, _P, _
                                _P, ctypes.c_size_t, _P]
 _lib.sa_cache_attn_workspace_bytes.argtypes = [_L, _I, _I, _I, _I]
 _lib.sa_cache_attn_workspace_bytes.restype = ctypes.c_size_t
+_lib.sa_debug_cache_attn_quit.argtypes = [_I]
+_lib.sa_debug_cache_attn_quit.restype = None
 _lib.sa_debug_cache_steps.argtypes = [_I, _I, _I, _I, _I]
 _lib.sa_debug_cache_steps.restype = _L
 _lib.sa_debug_wait_timeout.argtypes = [_I, _P]

@@ -1031,6 +1031,10 @@ sa_status sa_cache_read(void *k, void *v, int dtype, int64_t T, const int32_t *t
     return launch_cache_read(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
+static std::atomic<int> g_cache_attn_quit{-1};
+
+void sa_debug_cache_attn_quit(int worker) { g_cache_attn_quit.store(worker, std::memory_order_relaxed); }
+
 // The query side of an attention call over the cache.
 static sa_status check_group(int64_t T, int H, int group)
 {
@@ -1089,6 +1093,7 @@ sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T
     a.causal = causal != 0;
     a.window = std::min(window, 1 << 30);
     a.sm_scale = sm_scale;
+    a.quit = g_cache_attn_quit.load(std::memory_order_relaxed);
     return launch_cache_attn(tm_k, tm_v, a, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SA_OK
                                                                                                        : SA_ERR_CUDA;
 }

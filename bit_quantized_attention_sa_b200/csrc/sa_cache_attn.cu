@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
             }
     };
 
-    for (int i = 0; i < count; ++i) {
+    if (w == A.quit) ok = false;
+    for (int i = 0; ok && i < count; ++i) {
         if (i - window == 32) {
             cur = nxt;
             window += 32;
@@ -571,8 +572,12 @@ __global__ void __launch_bounds__(Sizes<D, NT>::kThreads, 1)
         if (lane == 0) record(6);
         // the tiles still in flight must land before the block's shared memory is given up
         for (int u = done; u < min(done + kSlots, 2 * count); ++u)
-            for (int i = 0; i < 1 << 20 && !mbar_try_wait(bars + 8 * uint32_t(u % kSlots), uint32_t(u / kSlots) & 1u); ++i) {
-            }
+            drain_wait(bars + 8 * uint32_t(u % kSlots), uint32_t(u / kSlots) & 1u);
+        // what others join with this warp's pieces is to be NaN, whichever of them it wrote
+        __syncwarp();
+        if (lane < kRows)
+            for (int slot = 2 * w; slot < 2 * w + 2; ++slot)
+                A.part[int64_t(slot) * S::kPart + kRows * D + lane] = __int_as_float(0x7fffffff);
     }
     if (!split && lane == 0) A.meta[2 * w] = make_int4(0, 0, 0, 0);
 }

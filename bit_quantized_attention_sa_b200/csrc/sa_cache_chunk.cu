@@ -61,7 +61,7 @@ constexpr uint32_t kMinusInf = 0xff800000u;
 
 constexpr int kBarQFull = 0, kBarKvFull = 2, kBarKvEmpty = kBarKvFull + kStages, kBarSFull = kBarKvEmpty + kStages,
               kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 1, kBarPvDone = kBarPFull + 2,
-              kBarOFull = kBarPvDone + 2, kBarOEmpty = kBarOFull + 2, kNumBars = kBarOEmpty + 2;
+              kBarOFull = kBarPvDone + 2, kBarOEmpty = kBarOFull + 2, kBarDrain = kBarOEmpty + 2, kNumBars = kBarDrain + 2;
 
 template <uint32_t NR>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NR)); }
@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
             mbar_init(bar(kBarPvDone + t), 1);
             mbar_init(bar(kBarOFull + t), 1);
             mbar_init(bar(kBarOEmpty + t), 4);
+            mbar_init(bar(kBarDrain + t), 1);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -476,6 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 const int nt = w.tiles(A);
                 for (int t = 0; t < nt && ok; ++t) wait(kBarQFull + t, q[t]++);
                 for (int j = 0; j < w.count && ok; ++j, ++g) {
+                    if (g == 1 && int(blockIdx.x) == A.quit) {
+                        ok = false;
+                        break;
+                    }
                     const uint32_t st = (2 * g) % kStages;
                     wait(kBarKvFull + st, ((2 * g) / kStages));
                     const uint64_t kd = sdesc(sbase + S::kOffKv + st * S::kTileBytes, 1024, SWZ_128B);
@@ -527,6 +532,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
                 }
                 for (int t = 0; t < nt; ++t) ++o[t];
             }
+        }
+        if (!ok && warp <= kWarpPV) {  // the products in flight must land before tensor memory is given up
+            if (lane == 0) *abort_flag = 1;
+            const uint32_t drain = bar(kBarDrain + warp - kWarpQK);
+            if (elect_one()) tc_commit(drain);
+            __syncwarp();
+            drain_wait(drain, 0);
         }
     } else if (warp >= kWarpConvert) {
         // ---------------------------------------------------------------- codes to fp16 tiles
@@ -872,6 +884,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const CacheAtt
     __syncthreads();
     tc_fence_after();
     if (warp == kWarpQK) tmem_dealloc(tmem, kTmemCols);
+    if (*abort_flag) {  // what others join with this block's pieces is to be NaN, whichever of them it wrote
+        static_assert(2 * kRowsSeg == kThreads, "a maximum for each thread");
+        A.part[int64_t(2 * blockIdx.x + threadIdx.x / kRowsSeg) * S::kPart + kRowsSeg * D + threadIdx.x % kRowsSeg] =
+            __int_as_float(0x7fffffff);
+    }
 }
 
 // Joins the pieces of the segment that worker blockIdx.x began and others went on with, in the

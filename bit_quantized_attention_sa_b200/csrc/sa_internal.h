@@ -182,6 +182,7 @@ struct CacheAttnArgs {
     int T = 0, B = 0, H = 0, G = 1, d = 0, max_pages = 0, num_pages = 0;  // H key/value heads, G query heads on each
     int causal = 1, window = 0;
     float sm_scale = 0.0f;
+    int quit = -1;  // a worker (warp of the one kernel, block of the other) that gives up as if a wait had expired
     // Set by the launcher, in the workspace.  For each worker meta[2 w] = {pieces of the segment that it
     // began and others went on with (0: none), slot of the first}, meta[2 w + 1] = {the sequence's first
     // token, head, first row of the segment, its rows}.

@@ -84,6 +84,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// A wait bounded by time alone (not by the abort flag): used to let this CTA's own
+// copies and MMAs land before it frees its memory.
+__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > SA_WAIT_LIMIT_NS) return false;
+    return true;
+}
+
 // ------------------------------------------------------------------ TMA
 
 // 2-D tiled bulk tensor load global -> shared, completion counted on `bar` in bytes.

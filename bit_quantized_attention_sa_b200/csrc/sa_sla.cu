@@ -44,16 +44,6 @@ constexpr int kStateFloats = kD * kStateCols;        // 17408 per key (or query)
 
 __device__ int g_sla_status;  // 0 = OK, 6 = a bounded wait expired
 
-// A wait bounded by time alone (not by the abort flag): used to let this CTA's own
-// copies and MMAs land before it frees its memory.
-__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity)
-{
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > SA_WAIT_LIMIT_NS) return false;
-    return true;
-}
-
 // hi keeps the sign, exponent and top 10 mantissa bits (exact in TF32); lo = x - hi exactly.
 __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
 

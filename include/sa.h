@@ -394,6 +394,13 @@ sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T
  * that it refuses, or no device). */
 size_t sa_cache_attn_workspace_bytes(int64_t T, int B, int H, int group, int d);
 
+/* Debug (host only): in later sa_cache_attn calls of the process this worker (a block of the
+ * kernel of many rows, a warp of the other) gives up after its first work as if a wait had expired,
+ * for tests of failure detection; -1: none.  Such a call sets SA_ERR_DEVICE_TIMEOUT; of the rows
+ * that the worker has part in, those that it begins are left as they were or NaN, those that it goes
+ * on with are NaN. */
+void sa_debug_cache_attn_quit(int worker);
+
 /* Debug (host only): the steps of 256 rows by 128 keys that sa_cache_attn's tensor-core kernel
  * takes for each key/value head of a sequence of n queries over len cached tokens (-1: refused). */
 int64_t sa_debug_cache_steps(int n, int len, int group, int causal, int window);
