@@ -23,12 +23,6 @@ if not os.path.exists(_LIB_PATH):
 
 _lib = ctypes.CDLL(_LIB_PATH)
 
-try:
-    from . import _sa_torch  # the serving calls' torch side, which calls the same library
-except ImportError as e:
-    raise ImportError(f"_sa_torch.so in {_PKG} is missing or does not fit this PyTorch: build it with"
-                      " `python -m bit_quantized_attention_sa_b200.build`") from e
-
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -432,7 +426,22 @@ def sa_sla_fwd(q, k, v, classes, sm_scale: float | None = None, phi: int = SA_PH
 
 # These calls recur for every layer of a decoding step, so their checks and marshalling are
 # compiled (csrc/sa_torch.cpp); wrong tensors raise ValueError there, a library status SAError.
-_sa_torch.set_error(SAError)
+# That side fits one PyTorch build, the library any, so it is loaded by the first such call.
+_serving = None
+
+
+def _torch_side():
+    global _serving
+    if _serving is None:
+        try:
+            from . import _sa_torch
+        except ImportError as e:
+            raise ImportError(f"_sa_torch.so in {_PKG} is missing or does not fit this PyTorch: build it with"
+                              " `python -m bit_quantized_attention_sa_b200.build`") from e
+        _sa_torch.set_error(SAError)
+        _serving = _sa_torch
+    return _serving
+
 
 CACHE_PAGE = 64  # tokens of a page
 _ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
@@ -485,21 +494,21 @@ def sa_rope(q, k, pos, freqs, rot: int | None = None, interleaved: bool = False,
         if len(outs) != (1 if k is None else 2):
             raise ValueError("out must match q and k")
         out_q, out_k = outs[0], outs[-1] if k is not None else None
-    return _sa_torch.rope(q, k, pos, freqs, rot, interleaved, sections, amplitude, inverse, out_q, out_k)
+    return _torch_side().rope(q, k, pos, freqs, rot, interleaved, sections, amplitude, inverse, out_q, out_k)
 
 
 def sa_cache_append(cache, k, v, tok_start, kv_lens, page_table) -> None:
     """Writes the new tokens k, v [T, heads, d] (bf16 or fp16; token strides as from a slice of
     a fused projection) into the cache.  kv_lens int32 [B] counts each sequence's tokens
     including the new ones, which are rows tok_start[b] .. tok_start[b + 1] - 1."""
-    _sa_torch.append(*cache, k, v, tok_start, kv_lens, page_table)
+    _torch_side().append(*cache, k, v, tok_start, kv_lens, page_table)
 
 
 def sa_cache_read(cache, tokens: int, tok_start, kv_lens, page_table, dtype=torch.bfloat16):
     """The values (k, v), each [tokens, heads, d] of dtype (bf16, fp16 or fp32), of the tokens
     at tok_start / kv_lens: the last tok_start[b + 1] - tok_start[b] of each sequence.  Rows that
     belong to no sequence are not written."""
-    return _sa_torch.read(*cache, tokens, tok_start, kv_lens, page_table, dtype)
+    return _torch_side().read(*cache, tokens, tok_start, kv_lens, page_table, dtype)
 
 
 def sa_cache_attn(cache, q, tok_start, kv_lens, page_table, causal: bool = True, window: int = 0,
@@ -511,7 +520,7 @@ def sa_cache_attn(cache, q, tok_start, kv_lens, page_table, causal: bool = True,
     other share one.  Returns o [T, query heads, d], and lse fp32 [T, query heads] with
     return_lse; 0 and -inf for a query that sees nothing.  Rows that belong to no sequence are
     not written."""
-    return _sa_torch.attn(*cache, q, tok_start, kv_lens, page_table, causal, window, sm_scale, return_lse, out)
+    return _torch_side().attn(*cache, q, tok_start, kv_lens, page_table, causal, window, sm_scale, return_lse, out)
 
 
 def sa_debug_qk_s32(q_i8, k_i8, N: int):
