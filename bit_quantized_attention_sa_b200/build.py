@@ -35,6 +35,7 @@ NVCC_FLAGS = [
 
 
 TORCH_EXT = os.path.join(PKG, "_sa_torch.so")
+TORCH_EXT_FITS = os.path.join(BUILD, "_sa_torch.fits")  # what TORCH_EXT was built against
 
 
 def nvcc() -> str:
@@ -67,9 +68,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.run(cmd, check=True)
         os.replace(LIB + ".tmp", LIB)
     src = os.path.join(CSRC, "sa_torch.cpp")
-    if force or _stale(TORCH_EXT, [src, os.path.join(ROOT, "include", "sa.h"), __file__]):
+    if force or _stale(TORCH_EXT, [src, os.path.join(ROOT, "include", "sa.h"), __file__]) or not _torch_ext_fits():
         build_torch_ext(src)
     return LIB
+
+
+def _torch_ext_for() -> str:
+    """What the torch side depends on beside its sources: the PyTorch and Python that would load it
+    (looked up without importing PyTorch)."""
+    from importlib import metadata, util
+
+    where = util.find_spec("torch")
+    return f"torch {metadata.version('torch')} at {where.origin if where else None}, {sys.implementation.cache_tag}"
+
+
+def _torch_ext_fits() -> bool:
+    if not os.path.exists(TORCH_EXT_FITS):
+        return False
+    with open(TORCH_EXT_FITS) as f:
+        return f.read() == _torch_ext_for()
 
 
 def build_torch_ext(src: str) -> None:
@@ -89,6 +106,8 @@ def build_torch_ext(src: str) -> None:
                                                   "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     subprocess.run(cmd, check=True)
     os.replace(TORCH_EXT + ".tmp", TORCH_EXT)
+    with open(TORCH_EXT_FITS, "w") as f:
+        f.write(_torch_ext_for())
 
 
 def main(argv=None) -> int:

@@ -33,3 +33,22 @@ else:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_another_pytorch_has_it_rebuilt(libsa, tmp_path, monkeypatch):
+    from bit_quantized_attention_sa_b200 import build
+
+    built = []
+    monkeypatch.setattr(build, "build_torch_ext", built.append)
+    build.build()
+    assert not built                                     # fresh, as the fixture left it
+    note = tmp_path / "fits"
+    monkeypatch.setattr(build, "TORCH_EXT_FITS", str(note))
+    build.build()
+    assert len(built) == 1                               # nobody knows what it was built against
+    note.write_text(build._torch_ext_for())
+    build.build()
+    assert len(built) == 1
+    monkeypatch.setattr("importlib.metadata.version", lambda name: "1.0.0")
+    build.build()
+    assert len(built) == 2
