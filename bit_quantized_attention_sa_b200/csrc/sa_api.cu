@@ -433,17 +433,25 @@ static void varlen_groups(int nseq, const int *seqlens, int H, std::vector<int> 
 
 static bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// The sizes of a call on the cache.
+static sa_status check_cache_sizes(int64_t T, int B, int H, int d)
+{
+    if (T < 0 || B < 1 || H < 1) return SA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return SA_ERR_UNSUPPORTED;
+    if (T > (1 << 30) || B > (1 << 20) || H > 65535 || (T / kPage + 2 * int64_t(B)) * H > INT_MAX) return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
 // What the calls on the cache share: sizes, the cache's and the sequences' arrays.
 static sa_status check_cache(int64_t T, int B, int H, int d, int max_pages, int num_pages, const void *tok_start,
                              const void *kv_lens, const void *table, const void *k_codes, const void *k_scale,
                              const void *v_codes, const void *v_scale)
 {
-    if (T < 0 || B < 1 || H < 1 || max_pages < 1 || num_pages < 1) return SA_ERR_INVALID_ARG;
-    if (d != 64 && d != 128) return SA_ERR_UNSUPPORTED;
+    if (max_pages < 1 || num_pages < 1) return SA_ERR_INVALID_ARG;
+    const sa_status r = check_cache_sizes(T, B, H, d);
+    if (r != SA_OK) return r;
     // lines of 128 bytes are a 32-bit TMA coordinate; positions and grid dimensions likewise
-    if (T > (1 << 30) || B > (1 << 20) || H > 65535 || max_pages > (1 << 30) / kPage ||
-        int64_t(num_pages) * H > (int64_t(INT_MAX) * 2) / d || (T / kPage + 2 * int64_t(B)) * H > INT_MAX)
-        return SA_ERR_UNSUPPORTED;
+    if (max_pages > (1 << 30) / kPage || int64_t(num_pages) * H > (int64_t(INT_MAX) * 2) / d) return SA_ERR_UNSUPPORTED;
     if (T == 0) return SA_OK;
     for (const void *p : {tok_start, kv_lens, table, k_codes, k_scale, v_codes, v_scale})
         if (!p) return SA_ERR_INVALID_ARG;
@@ -1100,7 +1108,7 @@ sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T
 
 size_t sa_cache_attn_workspace_bytes(int64_t T, int B, int H, int group, int d)
 {
-    if (T < 0 || B < 1 || H < 1 || (d != 64 && d != 128) || check_group(T, H, group) != SA_OK) return 0;
+    if (check_cache_sizes(T, B, H, d) != SA_OK || check_group(T, H, group) != SA_OK) return 0;
     const int sms = device_sms();
     return sms < 1 ? 0 : cache_attn_workspace(sms, T, B, group, d);
 }

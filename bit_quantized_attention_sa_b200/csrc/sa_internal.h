@@ -194,8 +194,8 @@ size_t cache_attn_workspace(int sms, int64_t T, int B, int G, int d);
 cudaError_t launch_cache_attn(const CUtensorMap &tm_k, const CUtensorMap &tm_v, CacheAttnArgs a, void *workspace,
                               cudaStream_t st);
 cudaError_t read_and_clear_cache_attn_status(int *status);
-// The tensor-core kernel for many rows (sa_cache_chunk.cu), called by launch_cache_attn, which
-// joins split segments afterwards.
+// The tensor-core kernel for many rows (sa_cache_chunk.cu), called by launch_cache_attn, and the
+// joining of its split segments.
 constexpr int kCacheChunkMaxSeqs = 4096;
 size_t cache_chunk_part_bytes(int sms, int d);
 cudaError_t launch_cache_chunk(const CacheAttnArgs &a, int sms, cudaStream_t st);

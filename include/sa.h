@@ -374,7 +374,8 @@ sa_status sa_cache_read(void *k, void *v, int dtype, int64_t T, const int32_t *t
 
 /* Attention of the T query tokens q [T, H * group, d] (SA_BF16 or SA_FP16, token stride q_tok)
  * over the cache, whose tokens include the queries' own (append first).  Query head h reads
- * key/value head h / group.  The query at position p sees the tokens t < kv_lens[b] with
+ * key/value head h / group (H * group <= 65535, T * group <= 2^30 and T * H * group <= 2^34, else
+ * SA_ERR_UNSUPPORTED).  The query at position p sees the tokens t < kv_lens[b] with
  * t <= p (causal != 0) and t > p - window (window > 0; 0: no window).
  *   o [T, H * group, d] (contiguous, dtype, apart from q in memory) = sum_t softmax_t(q . k_t * sm_scale) v_t, and lse
  *   fp32 [T, H * group] (or NULL) = log sum_t exp(q . k_t * sm_scale); a query that sees
