@@ -44,35 +44,42 @@ struct Place {
     bool first;  // the sequence's first slot
 };
 
-template <int kThreads>
+template <int kThreads, bool MANY>
 __device__ __forceinline__ bool find_place(const CacheArgs &A, int slot, Place &P)
 {
     // base is increasing in b: b is the last one whose base is at or below the slot; the thread
-    // that looks at it has the rest of what there is to know already on its way.  Where offsets
-    // decrease, the count names some other sequence, which finds that the slot is not its own.
+    // that looks at it has the rest of what there is to know already on its way.  MANY, more sequences
+    // than threads: first, each round leaves those between two that the threads looked at (where every slot
+    // looked through all, 65536 tokens of as many sequences took 16 ms, now 0.8; one round costs 1 % of
+    // append-prompts, so fewer sequences have kernels without it).  Where offsets decrease, the count names
+    // some other sequence, which finds that the slot is not its own.
     __shared__ int found[4];
-    int below = 0;
-    for (int i = 0; i < A.B; i += kThreads) {
-        const int b = i + int(threadIdx.x);
-        int ts = 0, te = 0, len = 0;
-        if (b < A.B) {
-            ts = A.tok_start[b];
-            te = A.tok_start[b + 1];
-            len = A.kv_lens[b];
+    int from = 0, to = A.B;
+    if constexpr (MANY) {
+        while (to - from > kThreads) {
+            const int step = (to - from + kThreads - 1) / kThreads, b = from + int(threadIdx.x) * step;
+            const int c = __syncthreads_count(b < to && A.tok_start[b] / kPage + 2 * b <= slot);
+            if (c == 0) return false;
+            from += (c - 1) * step;
+            to = min(to, from + step);
         }
-        const bool in = b < A.B && ts / kPage + 2 * b <= slot;
-        const int c = __syncthreads_count(in);
-        if (int(threadIdx.x) == c - 1) {
-            found[0] = b;
-            found[1] = ts;
-            found[2] = te;
-            found[3] = len;
-        }
-        below += c;
-        if (c < kThreads) break;
+    }
+    const int b = from + int(threadIdx.x);
+    int ts = 0, te_b = 0, len = 0;
+    if (b < to) {
+        ts = A.tok_start[b];
+        te_b = A.tok_start[b + 1];
+        len = A.kv_lens[b];
+    }
+    const int c = __syncthreads_count(b < to && ts / kPage + 2 * b <= slot);
+    if (int(threadIdx.x) == c - 1) {
+        found[0] = b;
+        found[1] = ts;
+        found[2] = te_b;
+        found[3] = len;
     }
     __syncthreads();
-    if (below == 0) return false;
+    if (c == 0) return false;
     P.b = found[0];
     P.ts = found[1];
     const int te = found[2];
@@ -182,7 +189,7 @@ __device__ __forceinline__ float new_scale(uint32_t bits, float s_old, bool olde
     return !older || s_new > s_old || s_new != s_new ? s_new : s_old;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool MANY>
 __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) cache_append_kernel(const CacheArgs A)
 {
     constexpr int kThreads = 4 * D, kHalf = kThreads / 2;
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) cache_append_kernel(con
     __shared__ uint32_t most[2][kThreads / 32];
     chain_begin();
     Place P;
-    if (!find_place<kThreads>(A, int(blockIdx.x) / A.head_cuts, P) || P.page < 0) return;
+    if (!find_place<kThreads, MANY>(A, int(blockIdx.x) / A.head_cuts, P) || P.page < 0) return;
     const int side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
     const int h_lo = int(blockIdx.x) % A.head_cuts * A.heads_per_block, h_hi = min(A.H, h_lo + A.heads_per_block);
     const int row_lo = P.lo - P.block * kPage, row_hi = P.hi - P.block * kPage;  // new rows
@@ -246,13 +253,13 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) cache_append_kernel(con
 // nothing waits for threads that have no value, and reads the values again if they are more rows
 // than it holds.  64 sequences of one token, 8 heads of 128: 3.7 us instead of 9.5.
 constexpr int kFewTokens = 4, kFewWarps = 8;
-template <typename T, int D>
+template <typename T, int D, bool MANY>
 __global__ void __launch_bounds__(32 * kFewWarps) cache_append_few_kernel(const CacheArgs A)
 {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows at once
     chain_begin();
     Place P;
-    if (!find_place<32 * kFewWarps>(A, int(blockIdx.x) / A.head_cuts, P) || P.page < 0) return;
+    if (!find_place<32 * kFewWarps, MANY>(A, int(blockIdx.x) / A.head_cuts, P) || P.page < 0) return;
     const int lane = threadIdx.x & 31, unit = int(blockIdx.x) % A.head_cuts * kFewWarps + int(threadIdx.x >> 5);
     const int head = unit / 2, side = unit % 2;
     if (head >= A.H) return;
@@ -336,14 +343,15 @@ __device__ __forceinline__ void load_codes(const int8_t *p, float (&f)[N])
 }
 
 // Writes are most of it, so a thread takes as many codes as fill 16 bytes of the output.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheArgs A)
+constexpr int kReadThreads = 256;
+template <typename T, int D, bool MANY>
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const CacheArgs A)
 {
-    constexpr int kThreads = 256, kHalf = kThreads / 2, kCodes = 16 / int(sizeof(T)), kChunks = D / kCodes;
+    constexpr int kThreads = kReadThreads, kHalf = kThreads / 2, kCodes = 16 / int(sizeof(T)), kChunks = D / kCodes;
     constexpr int kPer = kPage * kChunks / kHalf;
     chain_begin();
     Place P;
-    if (!find_place<kThreads>(A, int(blockIdx.x) / A.H, P)) return;
+    if (!find_place<kThreads, MANY>(A, int(blockIdx.x) / A.H, P)) return;
     const int head = int(blockIdx.x) % A.H, side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
     T *dst = static_cast<T *>(const_cast<void *>(side ? A.v : A.k));
     if (!dst) return;
@@ -379,7 +387,8 @@ cudaError_t append_for(CacheArgs a, cudaStream_t st)
 {
     if (a.T <= int64_t(kFewTokens) * a.B) {
         a.head_cuts = int(cdiv(2 * int64_t(a.H), kFewWarps));
-        return launch_chained(cache_append_few_kernel<T, D>, dim3(unsigned(slots_of(a) * a.head_cuts)), 32 * kFewWarps, 0, st, a);
+        return launch_chained(a.B > 32 * kFewWarps ? cache_append_few_kernel<T, D, true> : cache_append_few_kernel<T, D, false>,
+                              dim3(unsigned(slots_of(a) * a.head_cuts)), 32 * kFewWarps, 0, st, a);
     }
     // several heads a block where there are blocks enough to fill the SMs several times over
     const int64_t blocks = (a.T / kPage + a.B) * int64_t(a.H);  // about so many are not empty
@@ -387,15 +396,17 @@ cudaError_t append_for(CacheArgs a, cudaStream_t st)
     a.head_cuts = int(cdiv(a.H, a.heads_per_block));
     const int64_t grid = slots_of(a) * a.head_cuts;
     if (grid > INT_MAX) return cudaErrorInvalidValue;
-    return launch_chained(cache_append_kernel<T, D>, dim3(unsigned(grid)), 4 * D, 0, st, a);
+    return launch_chained(a.B > 4 * D ? cache_append_kernel<T, D, true> : cache_append_kernel<T, D, false>, dim3(unsigned(grid)),
+                          4 * D, 0, st, a);
 }
 
-template <typename T>
+template <typename T, int D>
 cudaError_t read_for(const CacheArgs &a, cudaStream_t st)
 {
     const int64_t grid = slots_of(a) * a.H;
     if (grid > INT_MAX) return cudaErrorInvalidValue;
-    return launch_chained(a.d == 128 ? cache_read_kernel<T, 128> : cache_read_kernel<T, 64>, dim3(unsigned(grid)), 256, 0, st, a);
+    return launch_chained(a.B > kReadThreads ? cache_read_kernel<T, D, true> : cache_read_kernel<T, D, false>,
+                          dim3(unsigned(grid)), kReadThreads, 0, st, a);
 }
 
 }  // namespace
@@ -408,9 +419,9 @@ cudaError_t launch_cache_append(const CacheArgs &a, int dtype, cudaStream_t st)
 
 cudaError_t launch_cache_read(const CacheArgs &a, int dtype, cudaStream_t st)
 {
-    if (dtype == 0) return read_for<__nv_bfloat16>(a, st);
-    if (dtype == 1) return read_for<__half>(a, st);
-    return read_for<float>(a, st);
+    if (dtype == 0) return a.d == 128 ? read_for<__nv_bfloat16, 128>(a, st) : read_for<__nv_bfloat16, 64>(a, st);
+    if (dtype == 1) return a.d == 128 ? read_for<__half, 128>(a, st) : read_for<__half, 64>(a, st);
+    return a.d == 128 ? read_for<float, 128>(a, st) : read_for<float, 64>(a, st);
 }
 
 cudaError_t read_and_clear_cache_status(int *status)
