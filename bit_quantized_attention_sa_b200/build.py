@@ -75,11 +75,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def _torch_ext_for() -> str:
     """What the torch side depends on beside its sources: the PyTorch and Python that would load it
-    (looked up without importing PyTorch)."""
+    (looked up without importing PyTorch, unless nothing but PyTorch itself knows its version)."""
     from importlib import metadata, util
 
     where = util.find_spec("torch")
-    return f"torch {metadata.version('torch')} at {where.origin if where else None}, {sys.implementation.cache_tag}"
+    try:
+        version = metadata.version("torch")
+    except metadata.PackageNotFoundError:
+        import torch
+
+        version = torch.__version__
+    return f"torch {version} at {where.origin if where else None}, {sys.implementation.cache_tag}"
 
 
 def _torch_ext_fits() -> bool:

@@ -63,3 +63,41 @@ def test_a_million_sequences(libsa, cuda_ok):
         page = _i32(torch.repeat_interleave(table[busy, 0], new[busy])).long()
         assert bool(((x.float() - y).abs() <= 0.5001 * scale[page][:, :, None]).all())
     assert begin.elapsed_time(end) < 1000
+
+
+@pytest.mark.parametrize("B", [300, 2000])
+@pytest.mark.parametrize("how", ["falling", "some", "random"])
+def test_offsets_out_of_order(libsa, cuda_ok, B, how):
+    """Whatever the offsets are, each page holds its own sequence's tokens or is as it was, and sequences
+    whose offsets fall are reported."""
+    gen = torch.Generator().manual_seed(B)
+    H, d, T = 1, 64, 2 * B
+    starts = torch.arange(B + 1) * 2
+    if how == "falling":
+        starts = starts.flip(0)
+    elif how == "some":
+        at = torch.randperm(B, generator=gen)[:20]
+        starts[at] = torch.randint(0, T, (20,), generator=gen)
+    else:
+        starts = torch.randint(-5, T + 5, (B + 1,), generator=gen)
+    new = starts[1:] - starts[:-1]
+    valid = (starts[:-1] >= 0) & (new >= 0) & (starts[1:] <= T) & (new <= 64)
+    lens = torch.where(valid, new, 1)                                   # a longer one would not fit its page
+    args = _i32(starts), _i32(lens), _i32(torch.arange(B)[:, None])
+    cache = libsa.sa_cache_alloc(B, H, d)
+    cache[1].fill_(-1.0)
+    k = torch.randn(T, H, d, device="cuda").half()
+    libsa.sa_cache_append(cache, k, k, *args)
+    assert libsa.sa_get_device_status() == 8
+    written = 0
+    for b in (cache[1][:, 0] != -1).nonzero()[:, 0].tolist():
+        if not valid[b]:
+            # only the last of its tokens is in the cache, as its length says, or none of another's
+            assert lens[b] == 1 and new[b] > 64 and starts[b] >= 0 and starts[b + 1] <= T
+            x = k[starts[b + 1] - 1:starts[b + 1], 0].float()
+        else:
+            x = k[starts[b]:starts[b + 1], 0].float()
+        s = x.abs().max() / torch.tensor(127.0, device="cuda")
+        assert cache[1][b, 0] == s and torch.equal(cache[0][b, 0, :x.shape[0]].float(), (x / s).round())
+        written += 1
+    assert written == 0 if how == "falling" else written > B // 2 if how == "some" else True
