@@ -11,8 +11,8 @@
 // maximum is taken on the bits of |x|, so a NaN or infinity reaches the scale and the block
 // reads back as NaN instead of hiding it.
 //
-// What bounds it: two bytes read and one written per value (68132 tokens, 16 heads of 64: 84 us,
-// 5.0 TB/s; reading them back as fp32 135 us, 5.2 TB/s); for one token a sequence, the
+// What bounds it: two bytes read and one written per value (68132 tokens, 16 heads of 64: 83 us,
+// 5.1 TB/s; reading them back as fp32 134 us, 5.2 TB/s); for one token a sequence, the
 // chain of dependent loads (sequence, page, scale).  One block of threads takes one block of
 // tokens and some heads, half of it the keys, half the values; a head's values stay in
 // registers between the maximum and the codes.
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) cache_append_kernel(con
 
 // The same for few new tokens a sequence: a warp takes one head's keys or values alone, so that
 // nothing waits for threads that have no value, and reads the values again if they are more rows
-// than it holds.  64 sequences of one token, 8 heads of 128: 3.7 us instead of 9.5.
+// than it holds.  64 sequences of one token, 8 heads of 128: 3.5 us instead of 9.5.
 constexpr int kFewTokens = 4, kFewWarps = 8;
 template <typename T, int D, bool MANY>
 __global__ void __launch_bounds__(32 * kFewWarps) cache_append_few_kernel(const CacheArgs A)

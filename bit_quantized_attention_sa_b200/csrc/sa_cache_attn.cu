@@ -17,8 +17,8 @@
 // p, relative to 2^m with m rounded up, is the sum of P before its rounding times a power of two.
 //
 // What bounds it: reading 2 d bytes for each cached token and head.  Measured, 4 sequences of
-// 70001 to 131072 tokens, 32 query heads on 8 of 128: 154 us for 900 MB, 5.9 TB/s (a plain copy
-// has 6.55), and 12 for the joining, some of it hidden.  So every warp is a worker
+// 70001 to 131072 tokens, 32 query heads on 8 of 128: 157 us for 900 MB, 5.7 TB/s (a plain copy
+// has 6.55), and 10 for the joining, some of it hidden.  So every warp is a worker
 // of its own with a ring of TMA tiles in shared memory (K and V of a block are 64 x d bytes
 // each), and the blocks of all (sequence, head, tile) segments, laid out one after another, are
 // cut into equal ranges, one for each worker, whatever the lengths.  A range may begin or end
@@ -47,7 +47,10 @@ namespace {
 // Rows of a sequence and head, on average, up to which this kernel takes a call; the others go to
 // the tensor-core kernel of sa_cache_chunk.cu.  Measured at d = 128, 8 heads (this kernel / that
 // one, us): 16 rows, 16 sequences of 4000 tokens 50 / 70, 64 of them 140 / 234, one of 60000
-// 70 / 76; 24 rows, which are read twice here: 78 / 71, 252 / 237, 85 / 77.
+// 70 / 76; 24 rows, which are read twice here: 78 / 71, 252 / 237, 85 / 77.  The average is all
+// that the host knows (lengths are on the device), so a long piece among single tokens stays here, each
+// of its tiles reading the sequence's blocks: 255 single tokens and 2000 over 8000 728 us, as two calls
+// 199 and 81; 63 and 500 over 4000 153, as two calls 65 and 41.
 constexpr int kFewRows = 16;
 constexpr float kPBits = 15.0f;
 // Blocks of one worker, two tiles each, are counted in 32 bits; a call of more (minutes of work) is left out.

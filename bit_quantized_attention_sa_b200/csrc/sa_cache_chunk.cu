@@ -9,9 +9,11 @@
 // What bounds it: at d = 128 a step costs each SM 2048 cycles of tensor core, 2048 of ex2 (32768
 // of them, 16 a cycle) and 2560 of shared memory (1024 for Q and K of S, 512 for V of P . V, 512 to
 // write the fp16 tiles, 512 for the codes in and out), so all three have to run at once.  Measured,
-// 1560 queries of 40 heads over 32760 tokens: 1010 us, 1037 TFLOP/s, 3600 cycles a step.  Shared
-// memory sets the pace: half the tile writes, or no copies of codes, would take 7 to 8 % off, no
-// exponentials at all nothing.  Who does what:
+// 1560 queries of 40 heads over 32760 tokens: 1004 us in a burst at 1965 MHz (1042 TFLOP/s, 3370 cycles
+// a step), 1177 us at the power limit (1570 MHz, 889 TFLOP/s).  No unit is full (tensor core 56 % of the
+// cycles, ex2 58 %): what sets the pace is the chain S - softmax - P . V with shared memory under it.
+// Taken out to see: the exponentials 5 % less, half the tile writes 8 %, the copies of codes 14 %.  Who
+// does what:
 //   * warps 0-3 and 4-7: softmax of tile A and B, a thread owning a row (its 128 scores of a step
 //     in registers): maximum, exponentials, P to tensor memory, rescaling of acc, epilogue;
 //   * warps 8-11: the codes, copied ahead from the pages (cp.async, each thread its own 16-byte

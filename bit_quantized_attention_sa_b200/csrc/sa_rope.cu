@@ -9,7 +9,7 @@
 // integer there, so a position of 2^20 loses nothing; sincospif then works on [-1, 1].
 //
 // What bounds it: reading and writing each value once (32760 tokens, 12 + 12 heads of 128 in bf16:
-// 72 us, 5.6 TB/s).  The sines of a token serve all its
+// 71 us, 5.7 TB/s).  The sines of a token serve all its
 // heads, so a block takes a few tokens of all heads (or a slice of the heads where there are
 // few tokens), puts the sines in shared memory once, and each thread keeps the eight pairs it
 // needs in registers while it walks the heads.

@@ -380,11 +380,14 @@ sa_status sa_cache_read(void *k, void *v, int dtype, int64_t T, const int32_t *t
  *   o [T, H * group, d] (contiguous, dtype, apart from q in memory) = sum_t softmax_t(q . k_t * sm_scale) v_t, and lse
  *   fp32 [T, H * group] (or NULL) = log sum_t exp(q . k_t * sm_scale); a query that sees
  *   nothing has o = 0 and lse = -inf.  sm_scale is positive and finite.
- * Products of fp16 operands (the codes and, up to a power of two for each row, q are exact;
- * softmax weights are rounded to fp16), sums and statistics in fp32.  The result does not
- * depend on timing.  workspace: device memory of at least
- * sa_cache_attn_workspace_bytes(T, B, H, group, d) bytes, which the call may overwrite and which no other call may use meanwhile; it need not
- * be set before or kept after. */
+ * Products of fp16 operands (the codes and, up to a power of two for each row, q are exact; a softmax
+ * weight times its block's value scale is rounded to fp16: off by at most 2^-11 of itself or 2^-31 of the
+ * largest such product that the row sees), sums and statistics in fp32.  The result does not depend on
+ * timing, and a row's not on blocks that it does not see.  One kernel takes the whole call, by its
+ * rows (T * group) to a sequence on average: long pieces among many single tokens are faster as a
+ * call of their own.  workspace: device memory of at least
+ * sa_cache_attn_workspace_bytes(T, B, H, group, d) bytes, which the call may overwrite and which no other
+ * call may use meanwhile; it need not be set before or kept after. */
 sa_status sa_cache_attn(const void *q, void *o, float *lse, int dtype, int64_t T, int64_t q_tok,
                         const int32_t *tok_start, const int32_t *kv_lens, const int32_t *page_table, int B,
                         int max_pages, const int8_t *k_codes, const float *k_scale, const int8_t *v_codes,
